@@ -16,9 +16,10 @@
  *
  * Conventions shared by every call:
  *   - Q, K, V, O (and dO, dQ, dK, dV) are bf16 tensors laid out [B, S, H, D],
- *     contiguous, D fastest.  D must be 128.
+ *     contiguous, D fastest.  D must be 128.  (The packed calls have their own
+ *     layout, a causal form and token strides: see wan_attn_varlen_fwd.)
  *   - lse is fp32 [B, H, S]: lse[b,h,i] = ln sum_j exp(q_i . k_j / sqrt(D)).
- *   - The softmax scale is fixed at 1/sqrt(D).  No mask, no dropout, no bias.
+ *   - The softmax scale is fixed at 1/sqrt(D).  No dropout, no bias.
  *   - Every pointer is a device pointer owned by the caller, 16-byte aligned.
  *     The library allocates no memory.  Outputs may not overlap inputs.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).  Calls
@@ -351,6 +352,114 @@ WAN_ATTN_API int wan_attn_fwd_q8(const void* q, const void* k, const void* v, vo
 WAN_ATTN_API int wan_attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
                                       const void* dO, const float* lse, void* dq, void* dk, void* dv,
                                       int B, int S, int H, int D, void* stream);
+
+/*
+ * Packed attention, bf16: N sequences of different lengths laid end to end on
+ * one token axis, without padding (clips of several sizes in one training
+ * batch; prompts of a serving step), full or causal, with grouped heads.
+ * Sequence n owns rows cu_q[n] .. cu_q[n+1]-1 of q and o and rows
+ * cu_k[n] .. cu_k[n+1]-1 of k and v; with Lq, Lk its two lengths,
+ *     o_i = sum_j p_ij v_j,  p_ij = exp(q_i . k_j / sqrt(D) - lse_i),
+ * over the keys j of the same sequence (full), or those with
+ * j <= i + (Lk - Lq) (causal: the last query sees every key, so Lq < Lk is the
+ * continuation of a sequence whose first Lk - Lq tokens are cached, and Lq = 1
+ * one generated token).  Query head h reads key/value head h / (H / Hkv).
+ *   q       : in,  bf16 [Tq, H, D], ldq elements from one token to the next
+ *   k, v    : in,  bf16 [Tk, Hkv, D], token strides ldk, ldv
+ *   o       : out, bf16 [Tq, H, D], contiguous
+ *   lse     : out, fp32 [H, Tq], natural log
+ *   cu_q, cu_k : in, int32 [N + 1] in device memory (4-byte aligned),
+ *             non-decreasing, 0 <= cu[0] and cu[N] <= T
+ *   Tq, Tk, N >= 0 (N >= 1); H a multiple of Hkv; D must be 128; token strides
+ *   multiples of 8, at least H D or Hkv D (slices of a fused projection's
+ *   output need no copy).  Lengths of 0 are allowed.
+ * A row that sees no key gets o = 0 and lse = -inf.  Rows outside every
+ * sequence are not read into any result and their o and lse are left as they
+ * were.  Inside a sequence q, k, v must be finite.  Offsets outside [0, T] or
+ * decreasing are clipped, never followed.
+ * Accumulation is fp32; P is rounded to bf16 for P V, as in wan_attn_fwd;
+ * every exponential comes from the hardware exp2.
+ *   workspace, workspace_bytes : device memory, 256-byte aligned, of at least
+ *             wan_attn_varlen_fwd_workspace_size bytes (0 for most sizes: the
+ *             pointer may then be NULL).  Needed where few query rows face
+ *             many keys: a sequence's keys are then split over several CTAs
+ *             whose partial results are joined.
+ * Other conventions and errors as wan_attn_fwd.
+ */
+WAN_ATTN_API size_t wan_attn_varlen_fwd_workspace_size(int N, int Tq, int Tk, int H, int Hkv, int D);
+WAN_ATTN_API int wan_attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
+                                     const int* cu_q, const int* cu_k, int N, int Tq, int Tk, int H, int Hkv,
+                                     int D, int64_t ldq, int64_t ldk, int64_t ldv, int causal, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
+ * Packed attention backward, bf16: gradients of sum(O * dO).
+ *   q, k, v, cu_q, cu_k, strides, causal : as in the forward
+ *   o, dO    : in,  bf16 [Tq, H, D], contiguous;  lse : in, fp32 [H, Tq]
+ *   dq       : out, bf16 [Tq, H, D], token stride lddq
+ *   dk, dv   : out, bf16 [Tk, Hkv, D], token strides lddk, lddv (each the sum
+ *              over the query heads of its group)
+ *   workspace, workspace_bytes : 256-byte aligned, at least
+ *              wan_attn_varlen_bwd_workspace_size bytes
+ * Rows of a sequence that no query sees get zero gradients; rows outside every
+ * sequence are left as they were.  dQ (and dK, dV where few key tiles make the
+ * call split them) is summed in fp32 in no fixed order, as in wan_attn_bwd.
+ */
+WAN_ATTN_API size_t wan_attn_varlen_bwd_workspace_size(int N, int Tq, int Tk, int H, int Hkv, int D);
+WAN_ATTN_API int wan_attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                                     const float* lse, void* dq, void* dk, void* dv, const int* cu_q,
+                                     const int* cu_k, int N, int Tq, int Tk, int H, int Hkv, int D, int64_t ldq,
+                                     int64_t ldk, int64_t ldv, int64_t lddq, int64_t lddk, int64_t lddv,
+                                     int causal, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The int8 linear layer: 8-bit integers with a scale per row, for activations
+ * X [M, K] a scale per token and for a weight W [N, K] one per output channel
+ * (the same quantiser):
+ *     s[m] = absmax_k |X[m,k]| / 127,  c[m,k] = rint(127 X[m,k] / absmax)
+ * (round half to even of the exact quotient; codes in [-127, 127]; s = 1 and
+ * c = 0 for a zero row; a row that holds an infinity or a NaN gets s = NaN and
+ * c = 0, so that it shows in every result that uses it)
+ *     Y[m,n] = bf16(s_x[m] s_w[n] sum_k cx[m,k] cw[n,k] + bias[n])
+ * with exact int32 sums.  K must be a multiple of 16, 16 <= K <= 131072 (the
+ * sums' range), N a multiple of 8, M >= 0.  Code rows are K contiguous bytes;
+ * pointers 16-byte aligned, scales 4-byte, outputs overlap no input.
+ */
+/* x bf16 [M, K], ldx elements (a multiple of 8) from row to row -> codes int8 [M, K], scales fp32 [M]. */
+WAN_ATTN_API int wan_int8_quantize_rows(const void* x, void* codes, float* scales, int M, int K, int64_t ldx,
+                                        void* stream);
+
+/* Reads 8-bit rows back: x bf16 [M, K] = bf16(scales[m] * codes[m,k]). */
+WAN_ATTN_API int wan_int8_dequantize_rows(const void* codes, const float* scales, void* x, int M, int K,
+                                          void* stream);
+
+/*
+ * y bf16 [M, N] from a_codes int8 [M, K], a_scales fp32 [M], b_codes int8
+ * [N, K], b_scales fp32 [N] and bias bf16 [N] (16-byte aligned; NULL = none).
+ */
+WAN_ATTN_API int wan_int8_gemm(const void* a_codes, const float* a_scales, const void* b_codes,
+                               const float* b_scales, const void* bias, void* y, int M, int N, int K, void* stream);
+
+/*
+ * The whole layer: quantises x into codes and scales, then multiplies.  codes
+ * int8 [M, K] and scales fp32 [M] are outputs: kept, they are the layer's
+ * 8-bit activation checkpoint (half of bf16's bytes) for the backward below.
+ */
+WAN_ATTN_API int wan_int8_linear(const void* x, const void* w_codes, const float* w_scales, const void* bias,
+                                 void* y, void* codes, float* scales, int M, int N, int K, int64_t ldx,
+                                 void* stream);
+
+/*
+ * The layer's backward from 8-bit operands (straight through the rounding):
+ *     dW[n,k] = sum_m dY[m,n] s_x[m] cx[m,k]     (dw bf16 [N, K], from the checkpoint)
+ *     dX[m,k] = sum_n dY[m,n] s_w[n] cw[n,k]     (dx bf16 [M, K], from the weight's codes)
+ * dy bf16 [M, N].  Each code times its scale is rounded to bf16 for the tensor
+ * core; sums are fp32.  M = 0 gives dW = 0.
+ */
+WAN_ATTN_API int wan_int8_grad_weight(const void* dy, const void* codes, const float* scales, void* dw, int M,
+                                      int N, int K, void* stream);
+WAN_ATTN_API int wan_int8_grad_input(const void* dy, const void* w_codes, const float* w_scales, void* dx, int M,
+                                     int N, int K, void* stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device status word:

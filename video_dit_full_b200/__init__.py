@@ -7,5 +7,7 @@ from .wan_attn import (CP_HEADS_TO_SEND, CP_RECV_TO_HEADS, CP_RECV_TO_SEQ, CP_SE
                        WanAttnError, bwd, bwd_workspace_size, check_status, cp_accumulate, cp_layout, cp_merge,
                        block_sparse_workspace_size, cross_bwd, cross_bwd_workspace_size, cross_fwd, fp8_gemm,
                        fp8_linear, fp8_quantize_rows, fwd_block_sparse,
-                       fp8_quantize_tensor, fwd, fwd_q8, fwd_q8_workspace_size, lib,
-                       q8_workspace_views, selftest_wait_timeout, set_wait_budget_ns, sync_status)
+                       fp8_quantize_tensor, fwd, fwd_q8, fwd_q8_workspace_size, int8_dequantize_rows,
+                       int8_gemm, int8_grad_input, int8_grad_weight, int8_linear, int8_quantize_rows, lib,
+                       q8_workspace_views, selftest_wait_timeout, set_wait_budget_ns, sync_status,
+                       varlen_bwd, varlen_bwd_workspace_size, varlen_fwd, varlen_fwd_workspace_size)

@@ -364,6 +364,117 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* o, const v
                : WAN_ATTN_ERR_CUDA;
 }
 
+// Shape, stride, alignment and overlap checks of the packed attention calls.  A tensor without
+// rows may have a null pointer.
+struct Packed {
+    const void* ptr;
+    long long rows, ld;
+    int heads;
+    bool out;
+    Range range() const {
+        return rows > 0 ? range_of(ptr, (size_t(rows - 1) * ld + size_t(heads) * 128) * 2) : Range{0, 0};
+    }
+};
+
+// Two tensors may interleave (slices of one fused [T, (H + 2 Hkv) D] buffer: the same token stride,
+// heads beside each other); otherwise their ranges must be apart.
+bool packed_clash(const Packed& a, const Packed& b) {
+    if (!overlaps(a.range(), b.range())) return false;
+    if (a.ld != b.ld) return true;
+    const long long ld = a.ld * 2, da = static_cast<long long>(a.heads) * 256, db = static_cast<long long>(b.heads) * 256;
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.ptr), pb = reinterpret_cast<uintptr_t>(b.ptr);
+    const long long gap = pa <= pb ? static_cast<long long>((pb - pa) % ld)              // a's row, then b's ...
+                                   : (ld - static_cast<long long>((pa - pb) % ld)) % ld;
+    return gap < da || gap + db > ld;                                                    // ... then a's next row
+}
+
+int check_packed(int N, int Tq, int Tk, int H, int Hkv, int D) {
+    if (N < 1 || Tq < 0 || Tk < 0 || H < 1 || Hkv < 1 || D < 1 || H % Hkv) return WAN_ATTN_ERR_INVALID_ARG;
+    if (D != 128) return WAN_ATTN_ERR_UNSUPPORTED;
+    if (H > 65535 || N > (1 << 24)) return WAN_ATTN_ERR_INVALID_ARG;
+    const double lim = double(1ull << 40);
+    if (double(Tq) * H * D >= lim || double(Tk) * Hkv * D >= lim) return WAN_ATTN_ERR_INVALID_ARG;
+    return WAN_ATTN_OK;
+}
+
+int check_packed_tensors(const Packed* t, int n, const Range* plain_in, int n_in, const Range* plain_out, int n_out) {
+    for (int i = 0; i < n; ++i) {
+        if (t[i].rows == 0) continue;
+        if (!t[i].ptr || !aligned16(t[i].ptr)) return WAN_ATTN_ERR_INVALID_ARG;
+        if (t[i].ld < static_cast<long long>(t[i].heads) * 128 || (t[i].ld & 7)) return WAN_ATTN_ERR_INVALID_ARG;
+        if (double(t[i].ld) * t[i].rows >= double(1ull << 40)) return WAN_ATTN_ERR_INVALID_ARG;
+    }
+    for (int i = 0; i < n; ++i) {
+        if (!t[i].rows) continue;
+        for (int j = 0; j < n; ++j)
+            if (j != i && t[j].rows && (t[i].out || t[j].out) && packed_clash(t[i], t[j])) return WAN_ATTN_ERR_INVALID_ARG;
+        for (int j = 0; j < n_out; ++j)
+            if (overlaps(t[i].range(), plain_out[j])) return WAN_ATTN_ERR_INVALID_ARG;
+        for (int j = 0; t[i].out && j < n_in; ++j)
+            if (overlaps(t[i].range(), plain_in[j])) return WAN_ATTN_ERR_INVALID_ARG;
+    }
+    for (int a = 0; a < n_out; ++a) {
+        for (int j = 0; j < n_in; ++j)
+            if (overlaps(plain_out[a], plain_in[j])) return WAN_ATTN_ERR_INVALID_ARG;
+        for (int c = a + 1; c < n_out; ++c)
+            if (overlaps(plain_out[a], plain_out[c])) return WAN_ATTN_ERR_INVALID_ARG;
+    }
+    return WAN_ATTN_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Fields that the packed forward and backward share.  False if there is no status word.
+bool fill_packed(VarlenParams& p, const void* q, const void* k, const void* v, const int* cu_q, const int* cu_k, int N,
+                 int Tq, int Tk, int H, int Hkv, long long ldq, long long ldk, long long ldv, int causal) {
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    p.N = N;
+    p.Tq = Tq;
+    p.Tk = Tk;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.ldq = ldq;
+    p.ldk = ldk;
+    p.ldv = ldv;
+    p.causal = causal ? 1 : 0;
+    p.scale = static_cast<float>(1.0 / std::sqrt(128.0));
+    p.scale_log2 = static_cast<float>((1.0 / std::sqrt(128.0)) * 1.4426950408889634);
+    p.wait_budget_ns = wait_budget_ns();
+    p.status = device_status_word();
+    return p.status != nullptr;
+}
+
+// Shapes of the int8 linear calls: M >= 0 rows, K % 16 == 0, 16 <= K <= 131072, N % 8 == 0 (>= 8).
+int check_int8_shape(int M, int N, int K) {
+    if (M < 0 || K < 16 || (K & 15) || K > 131072 || N < 8 || (N & 7)) return WAN_ATTN_ERR_INVALID_ARG;
+    const double lim = double(1ull << 40);
+    if (double(M) * K >= lim || double(N) * K >= lim || double(M) * N >= lim) return WAN_ATTN_ERR_INVALID_ARG;
+    return WAN_ATTN_OK;
+}
+
+// No null pointer, alignment `mask` + 1 each, and no output range over any other range.
+struct Arg {
+    const void* ptr;
+    size_t bytes;
+    unsigned mask;
+    bool out;
+};
+int check_args(const Arg* a, int n) {
+    for (int i = 0; i < n; ++i)
+        if (!a[i].ptr || (reinterpret_cast<uintptr_t>(a[i].ptr) & a[i].mask)) return WAN_ATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < n; ++j)
+            if (i != j && a[i].out && overlaps(range_of(a[i].ptr, a[i].bytes), range_of(a[j].ptr, a[j].bytes)))
+                return WAN_ATTN_ERR_INVALID_ARG;
+    return WAN_ATTN_OK;
+}
+
+int as_status(int rc) { return rc == 0 ? WAN_ATTN_OK : WAN_ATTN_ERR_CUDA; }
+
 }  // namespace
 
 extern "C" {
@@ -584,6 +695,151 @@ int wan_fp8_gemm(const void* a_codes, const float* a_scales, const void* b_codes
     if (!p.status) return WAN_ATTN_ERR_CUDA;
     return launch_fp8_gemm(ta, tb, tb_half, p, static_cast<cudaStream_t>(stream)) == 0 ? WAN_ATTN_OK
                                                                                      : WAN_ATTN_ERR_CUDA;
+}
+
+size_t wan_attn_varlen_fwd_workspace_size(int N, int Tq, int Tk, int H, int Hkv, int D) {
+    if (check_packed(N, Tq, Tk, H, Hkv, D) != WAN_ATTN_OK) return 0;
+    return 0;
+}
+
+int wan_attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float* lse, const int* cu_q,
+                        const int* cu_k, int N, int Tq, int Tk, int H, int Hkv, int D, int64_t ldq, int64_t ldk,
+                        int64_t ldv, int causal, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_packed(N, Tq, Tk, H, Hkv, D);
+    if (st != WAN_ATTN_OK) return st;
+    if (!cu_q || !cu_k || !aligned4(cu_q) || !aligned4(cu_k)) return WAN_ATTN_ERR_INVALID_ARG;
+    if (Tq == 0) return WAN_ATTN_OK;
+    if (!lse || !aligned16(lse)) return WAN_ATTN_ERR_INVALID_ARG;
+    const Packed t[] = {{q, Tq, ldq, H, false}, {k, Tk, ldk, Hkv, false}, {v, Tk, ldv, Hkv, false},
+                        {o, Tq, static_cast<long long>(H) * 128, H, true}};
+    const Range ins[] = {range_of(cu_q, size_t(N + 1) * 4), range_of(cu_k, size_t(N + 1) * 4)};
+    const Range outs[] = {range_of(lse, size_t(H) * Tq * 4)};
+    st = check_packed_tensors(t, 4, ins, 2, outs, 1);
+    if (st != WAN_ATTN_OK) return st;
+    VarlenFwdParams p{};
+    if (!fill_packed(p, q, k, v, cu_q, cu_k, N, Tq, Tk, H, Hkv, ldq, ldk, ldv, causal)) return WAN_ATTN_ERR_CUDA;
+    p.o = o;
+    p.lse = lse;
+    return as_status(launch_varlen_fwd(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t wan_attn_varlen_bwd_workspace_size(int N, int Tq, int Tk, int H, int Hkv, int D) {
+    if (check_packed(N, Tq, Tk, H, Hkv, D) != WAN_ATTN_OK) return 0;
+    return 256;
+}
+
+int wan_attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o, const void* dO, const float* lse,
+                        void* dq, void* dk, void* dv, const int* cu_q, const int* cu_k, int N, int Tq, int Tk, int H,
+                        int Hkv, int D, int64_t ldq, int64_t ldk, int64_t ldv, int64_t lddq, int64_t lddk,
+                        int64_t lddv, int causal, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_packed(N, Tq, Tk, H, Hkv, D);
+    if (st != WAN_ATTN_OK) return st;
+    if (!cu_q || !cu_k || !aligned4(cu_q) || !aligned4(cu_k)) return WAN_ATTN_ERR_INVALID_ARG;
+    if (Tq == 0 && Tk == 0) return WAN_ATTN_OK;
+    if (Tq > 0 && (!lse || !aligned16(lse))) return WAN_ATTN_ERR_INVALID_ARG;
+    const size_t need = wan_attn_varlen_bwd_workspace_size(N, Tq, Tk, H, Hkv, D);
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return WAN_ATTN_ERR_WORKSPACE;
+    const long long hd = static_cast<long long>(H) * 128;
+    const Packed t[] = {{q, Tq, ldq, H, false},  {k, Tk, ldk, Hkv, false},  {v, Tk, ldv, Hkv, false},
+                        {o, Tq, hd, H, false},   {dO, Tq, hd, H, false},    {dq, Tq, lddq, H, true},
+                        {dk, Tk, lddk, Hkv, true}, {dv, Tk, lddv, Hkv, true}};
+    const Range ins[] = {range_of(cu_q, size_t(N + 1) * 4), range_of(cu_k, size_t(N + 1) * 4),
+                         range_of(lse, size_t(H) * Tq * 4)};
+    const Range outs[] = {range_of(workspace, need)};
+    st = check_packed_tensors(t, 8, ins, 3, outs, 1);
+    if (st != WAN_ATTN_OK) return st;
+    VarlenBwdParams p{};
+    if (!fill_packed(p, q, k, v, cu_q, cu_k, N, Tq, Tk, H, Hkv, ldq, ldk, ldv, causal)) return WAN_ATTN_ERR_CUDA;
+    p.o = o;
+    p.dout = dO;
+    p.lse = lse;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.lddq = lddq;
+    p.lddk = lddk;
+    p.lddv = lddv;
+    return as_status(launch_varlen_bwd(p, static_cast<cudaStream_t>(stream)));
+}
+
+int wan_int8_quantize_rows(const void* x, void* codes, float* scales, int M, int K, int64_t ldx, void* stream) {
+    const int st = check_int8_shape(M, 8, K);
+    if (st != WAN_ATTN_OK || ldx < K || (ldx & 7) || double(ldx) * M >= double(1ull << 40)) return WAN_ATTN_ERR_INVALID_ARG;
+    if (M == 0) return WAN_ATTN_OK;
+    const Arg a[] = {{x, (size_t(M - 1) * ldx + K) * 2, 15, false}, {codes, size_t(M) * K, 15, true},
+                     {scales, size_t(M) * 4, 3, true}};
+    const int sa = check_args(a, 3);
+    if (sa != WAN_ATTN_OK) return sa;
+    return as_status(launch_int8_quant_rows(x, codes, scales, M, K, ldx, static_cast<cudaStream_t>(stream)));
+}
+
+int wan_int8_dequantize_rows(const void* codes, const float* scales, void* x, int M, int K, void* stream) {
+    const int st = check_int8_shape(M, 8, K);
+    if (st != WAN_ATTN_OK) return st;
+    if (M == 0) return WAN_ATTN_OK;
+    const Arg a[] = {{codes, size_t(M) * K, 15, false}, {scales, size_t(M) * 4, 3, false}, {x, size_t(M) * K * 2, 15, true}};
+    const int sa = check_args(a, 3);
+    if (sa != WAN_ATTN_OK) return sa;
+    return as_status(launch_int8_dequant_rows(codes, scales, x, M, K, static_cast<cudaStream_t>(stream)));
+}
+
+int wan_int8_gemm(const void* a_codes, const float* a_scales, const void* b_codes, const float* b_scales,
+                  const void* bias, void* y, int M, int N, int K, void* stream) {
+    const int st = check_int8_shape(M, N, K);
+    if (st != WAN_ATTN_OK) return st;
+    if (M == 0) return WAN_ATTN_OK;
+    const Arg a[] = {{a_codes, size_t(M) * K, 15, false}, {a_scales, size_t(M) * 4, 3, false},
+                     {b_codes, size_t(N) * K, 15, false}, {b_scales, size_t(N) * 4, 3, false},
+                     {y, size_t(M) * N * 2, 15, true},    {bias, size_t(N) * 2, 15, false}};
+    const int sa = check_args(a, bias ? 6 : 5);
+    if (sa != WAN_ATTN_OK) return sa;
+    return as_status(launch_int8_gemm(a_codes, a_scales, b_codes, b_scales, bias, y, M, N, K,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+int wan_int8_linear(const void* x, const void* w_codes, const float* w_scales, const void* bias, void* y, void* codes,
+                    float* scales, int M, int N, int K, int64_t ldx, void* stream) {
+    const int st = check_int8_shape(M, N, K);
+    if (st != WAN_ATTN_OK || ldx < K || (ldx & 7) || double(ldx) * M >= double(1ull << 40)) return WAN_ATTN_ERR_INVALID_ARG;
+    if (M == 0) return WAN_ATTN_OK;
+    const Arg a[] = {{x, (size_t(M - 1) * ldx + K) * 2, 15, false}, {w_codes, size_t(N) * K, 15, false},
+                     {w_scales, size_t(N) * 4, 3, false},           {y, size_t(M) * N * 2, 15, true},
+                     {codes, size_t(M) * K, 15, true},              {scales, size_t(M) * 4, 3, true},
+                     {bias, size_t(N) * 2, 15, false}};
+    const int sa = check_args(a, bias ? 7 : 6);
+    if (sa != WAN_ATTN_OK) return sa;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (launch_int8_quant_rows(x, codes, scales, M, K, ldx, s) != 0) return WAN_ATTN_ERR_CUDA;
+    return as_status(launch_int8_gemm(codes, scales, w_codes, w_scales, bias, y, M, N, K, s));
+}
+
+int wan_int8_grad_weight(const void* dy, const void* codes, const float* scales, void* dw, int M, int N, int K,
+                         void* stream) {
+    const int st = check_int8_shape(M, N, K);
+    if (st != WAN_ATTN_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (M == 0) {
+        if (!dw || !aligned16(dw)) return WAN_ATTN_ERR_INVALID_ARG;
+        return cudaMemsetAsync(dw, 0, size_t(N) * K * 2, s) == cudaSuccess ? WAN_ATTN_OK : WAN_ATTN_ERR_CUDA;
+    }
+    const Arg a[] = {{dy, size_t(M) * N * 2, 15, false}, {codes, size_t(M) * K, 15, false},
+                     {scales, size_t(M) * 4, 3, false}, {dw, size_t(N) * K * 2, 15, true}};
+    const int sa = check_args(a, 4);
+    if (sa != WAN_ATTN_OK) return sa;
+    return as_status(launch_int8_grad(dy, codes, scales, dw, N, K, M, 0, s));
+}
+
+int wan_int8_grad_input(const void* dy, const void* w_codes, const float* w_scales, void* dx, int M, int N, int K,
+                        void* stream) {
+    const int st = check_int8_shape(M, N, K);
+    if (st != WAN_ATTN_OK) return st;
+    if (M == 0) return WAN_ATTN_OK;
+    const Arg a[] = {{dy, size_t(M) * N * 2, 15, false}, {w_codes, size_t(N) * K, 15, false},
+                     {w_scales, size_t(N) * 4, 3, false}, {dx, size_t(M) * K * 2, 15, true}};
+    const int sa = check_args(a, 4);
+    if (sa != WAN_ATTN_OK) return sa;
+    return as_status(launch_int8_grad(dy, w_codes, w_scales, dx, M, K, N, 1, static_cast<cudaStream_t>(stream)));
 }
 
 int wan_attn_sync_status(void* stream) {

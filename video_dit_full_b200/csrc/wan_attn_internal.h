@@ -71,6 +71,28 @@ struct Fp8GemmParams {
     int* status;
 };
 
+// Packed attention: sequence n owns query rows [cu_q[n], cu_q[n+1]) and key rows [cu_k[n], cu_k[n+1]).
+struct VarlenParams {
+    const void *q, *k, *v;            // bf16 [Tq, H, 128], [Tk, Hkv, 128] with the token strides below
+    const int *cu_q, *cu_k;           // int32 [N + 1], device
+    int N, Tq, Tk, H, Hkv;
+    long long ldq, ldk, ldv;          // elements from one token to the next
+    int causal;
+    float scale, scale_log2;          // 1 / sqrt(D); the same times log2(e)
+    unsigned long long wait_budget_ns;
+    int* status;
+};
+struct VarlenFwdParams : VarlenParams {
+    void* o;                          // bf16 [Tq, H, 128]
+    float* lse;                       // fp32 [H, Tq]
+};
+struct VarlenBwdParams : VarlenParams {
+    const void *o, *dout;             // bf16 [Tq, H, 128]
+    const float* lse;                 // fp32 [H, Tq]
+    void *dq, *dk, *dv;               // bf16, token strides below
+    long long lddq, lddk, lddv;
+};
+
 // Device address of the status word on the current device (nullptr on failure).
 int* device_status_word();
 unsigned long long wait_budget_ns();
@@ -108,6 +130,19 @@ int launch_fp8_quant_tensor(const void* w, void* codes, float* scale2, long long
 // tb: W's map with 256-row boxes (1-CTA kernel); tb_half: 128-row boxes (CTA pairs).
 int launch_fp8_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tb_half, const Fp8GemmParams& p,
                     cudaStream_t stream);
+
+// Packed attention (attn_varlen_fwd.cu, attn_varlen_bwd.cu).  0 on success.
+int launch_varlen_fwd(const VarlenFwdParams& p, cudaStream_t stream);
+int launch_varlen_bwd(const VarlenBwdParams& p, cudaStream_t stream);
+
+// Int8 linear layer (int8_linear.cu) and its backward (int8_grad.cu).  0 on success.
+int launch_int8_quant_rows(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream);
+int launch_int8_dequant_rows(const void* codes, const float* scales, void* x, int M, int K, cudaStream_t stream);
+int launch_int8_gemm(const void* a_codes, const float* a_scales, const void* b_codes, const float* b_scales,
+                     const void* bias, void* y, int M, int N, int K, cudaStream_t stream);
+// out[r, c] = sum_t a(t, r) s[t] codes[t, c], a(t, r) = dy[t, r] (a_by_row = 0: dW) or dy[r, t] (1: dX)
+int launch_int8_grad(const void* dy, const void* codes, const float* scales, void* out, int rows, int cols, int terms,
+                     int a_by_row, cudaStream_t stream);
 
 // `to`: a map over the bf16 O [B, S, H, D] with 128-token boxes (the epilogue TMA-stores O through it).
 int launch_q8(const Q8QuantParams& qp, const CUtensorMap& tq8, const CUtensorMap& tk8, const CUtensorMap& tv8,

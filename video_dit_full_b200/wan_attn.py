@@ -19,6 +19,7 @@ STATUS = {0: "WAN_ATTN_OK", 1: "WAN_ATTN_ERR_INVALID_ARG", 2: "WAN_ATTN_ERR_UNSU
 
 # (name, restype, argtypes) of every entry point the header declares
 _P, _I, _Z, _U64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64, ctypes.c_void_p
+_L = ctypes.c_int64
 SIGNATURES = [
     ("wan_attn_fwd", _I, [_P, _P, _P, _P, _F, _I, _I, _I, _I, _P]),
     ("wan_attn_bwd_workspace_size", _Z, [_I, _I, _I, _I]),
@@ -37,6 +38,16 @@ SIGNATURES = [
     ("wan_attn_fwd_q8_workspace_size", _Z, [_I, _I, _I, _I]),
     ("wan_attn_fwd_q8", _I, [_P, _P, _P, _P, _F, _I, _I, _I, _I, _P, _Z, _P]),
     ("wan_attn_bwd_noalloc", _I, [_P, _P, _P, _P, _P, _F, _P, _P, _P, _I, _I, _I, _I, _P]),
+    ("wan_attn_varlen_fwd_workspace_size", _Z, [_I] * 6),
+    ("wan_attn_varlen_fwd", _I, [_P, _P, _P, _P, _F, _P, _P] + [_I] * 6 + [_L] * 3 + [_I, _P, _Z, _P]),
+    ("wan_attn_varlen_bwd_workspace_size", _Z, [_I] * 6),
+    ("wan_attn_varlen_bwd", _I, [_P] * 5 + [_F] + [_P] * 5 + [_I] * 6 + [_L] * 6 + [_I, _P, _Z, _P]),
+    ("wan_int8_quantize_rows", _I, [_P, _P, _F, _I, _I, _L, _P]),
+    ("wan_int8_dequantize_rows", _I, [_P, _F, _P, _I, _I, _P]),
+    ("wan_int8_gemm", _I, [_P, _F, _P, _F, _P, _P, _I, _I, _I, _P]),
+    ("wan_int8_linear", _I, [_P, _P, _F, _P, _P, _P, _F, _I, _I, _I, _L, _P]),
+    ("wan_int8_grad_weight", _I, [_P, _P, _F, _P, _I, _I, _I, _P]),
+    ("wan_int8_grad_input", _I, [_P, _P, _F, _P, _I, _I, _I, _P]),
     ("wan_attn_sync_status", _I, [_P]),
     ("wan_attn_status_string", ctypes.c_char_p, [_I]),
     ("wan_attn_set_wait_budget_ns", _U64, [_U64]),
@@ -332,6 +343,237 @@ def fp8_linear(x, w_codes, w_scale, stream=None):
     by fp8_quantize_tensor: the per-token quantiser, then the GEMM."""
     codes, scales = fp8_quantize_rows(x, stream=stream)
     return fp8_gemm(codes, scales, w_codes, w_scale, stream=stream)
+
+
+def _check_device(**tensors):
+    """Every tensor on the current device (the one whose stream and context the call uses)."""
+    import torch
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _check_packed(name, t, shape=None):
+    """A bf16 [T, H, D] CUDA tensor whose tokens may be strided; returns the token stride in elements."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, D]")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    T, H, D = t.shape
+    row = H * D
+    ld = t.stride(0) if T > 1 else max(row, t.stride(0) // 8 * 8)
+    if t.numel() and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D) or ld < row or ld % 8):
+        raise ValueError(f"{name} must hold each token's [H, D] contiguously, tokens a multiple of 8 elements apart")
+    return ld if t.numel() else row
+
+
+def _check_packed_call(q, k, v, cu_q, cu_k):
+    import torch
+    ldq, ldk = _check_packed("q", q), _check_packed("k", k)
+    ldv = _check_packed("v", v, k.shape)
+    Tq, H, D = q.shape
+    Tk, Hkv, Dk = k.shape
+    if Dk != D or Hkv < 1 or H % Hkv:
+        raise ValueError(f"k has shape {tuple(k.shape)}: its heads must divide q's {H}, its D be {D}")
+    for name, t in (("cu_q", cu_q), ("cu_k", cu_k)):
+        _check_plain(name, t, torch.int32)
+        if t.dim() != 1 or t.numel() < 2:
+            raise ValueError(f"{name} must be [sequences + 1]")
+    if cu_q.numel() != cu_k.numel():
+        raise ValueError("cu_q and cu_k must name the same number of sequences")
+    return cu_q.numel() - 1, Tq, Tk, H, Hkv, D, ldq, ldk, ldv
+
+
+def _workspace(need, given, device):
+    import torch
+    if given is None and need:
+        given = torch.empty(need, dtype=torch.uint8, device=device)
+    return (None, 0, None) if given is None else (given.data_ptr(), given.numel() * given.element_size(), given)
+
+
+def varlen_fwd_workspace_size(N, Tq, Tk, H, Hkv, D=128) -> int:
+    return lib().wan_attn_varlen_fwd_workspace_size(N, Tq, Tk, H, Hkv, D)
+
+
+def varlen_fwd(q, k, v, cu_q, cu_k, causal=False, o=None, lse=None, workspace=None, stream=None):
+    """O, LSE of packed sequences (``wan_attn_varlen_fwd``): q [Tq, H, D], k and v [Tk, Hkv, D] (tokens
+    may be strided), sequence n at rows cu_q[n]:cu_q[n+1] and cu_k[n]:cu_k[n+1] (int32, on the device).
+
+    Rows of a given o / lse outside every sequence keep what they held; without one they are undefined."""
+    import torch
+    N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv = _check_packed_call(q, k, v, cu_q, cu_k)
+    o = torch.empty((Tq, H, D), dtype=q.dtype, device=q.device) if o is None else o
+    _check_plain("o", o, torch.bfloat16, Tq * H * D)
+    lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device) if lse is None else lse
+    _check_plain("lse", lse, torch.float32, H * Tq)
+    _check_device(q=q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, o=o, lse=lse, workspace=workspace)
+    ws, ws_bytes, _keep = _workspace(varlen_fwd_workspace_size(N, Tq, Tk, H, Hkv, D), workspace, q.device)
+    _check("wan_attn_varlen_fwd",
+           lib().wan_attn_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                     cu_q.data_ptr(), cu_k.data_ptr(), N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv,
+                                     1 if causal else 0, ws, ws_bytes, _stream_ptr(stream)))
+    return o, lse
+
+
+def varlen_bwd_workspace_size(N, Tq, Tk, H, Hkv, D=128) -> int:
+    return lib().wan_attn_varlen_bwd_workspace_size(N, Tq, Tk, H, Hkv, D)
+
+
+def varlen_bwd(q, k, v, o, do, lse, cu_q, cu_k, causal=False, dq=None, dk=None, dv=None, workspace=None,
+               stream=None):
+    """dQ, dK, dV of sum(O * dO) for packed sequences (``wan_attn_varlen_bwd``); given dq, dk, dv may be strided."""
+    import torch
+    N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv = _check_packed_call(q, k, v, cu_q, cu_k)
+    _check_plain("o", o, torch.bfloat16, Tq * H * D)
+    _check_plain("do", do, torch.bfloat16, Tq * H * D)
+    _check_plain("lse", lse, torch.float32, H * Tq)
+    dq = torch.empty((Tq, H, D), dtype=q.dtype, device=q.device) if dq is None else dq
+    dk = torch.empty((Tk, Hkv, D), dtype=q.dtype, device=q.device) if dk is None else dk
+    dv = torch.empty((Tk, Hkv, D), dtype=q.dtype, device=q.device) if dv is None else dv
+    lddq = _check_packed("dq", dq, q.shape)
+    lddk, lddv = _check_packed("dk", dk, k.shape), _check_packed("dv", dv, k.shape)
+    _check_device(q=q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, o=o, do=do, lse=lse, dq=dq, dk=dk, dv=dv, workspace=workspace)
+    ws, ws_bytes, _keep = _workspace(varlen_bwd_workspace_size(N, Tq, Tk, H, Hkv, D), workspace, q.device)
+    _check("wan_attn_varlen_bwd",
+           lib().wan_attn_varlen_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                                     lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_q.data_ptr(),
+                                     cu_k.data_ptr(), N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv, lddq, lddk, lddv,
+                                     1 if causal else 0, ws, ws_bytes, _stream_ptr(stream)))
+    return dq, dk, dv
+
+
+def _check_matrix(name, t, dtype, cols=None):
+    """A contiguous 2-D CUDA tensor; returns its shape."""
+    _check_plain(name, t, dtype)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if cols is not None and t.shape[1] != cols:
+        raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
+    return tuple(t.shape)
+
+
+def _check_activations(x):
+    """bf16 [M, K] whose rows may be strided; returns M, K and the row stride in elements."""
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.bfloat16:
+        raise TypeError("x must be a bfloat16 CUDA tensor")
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    ld = x.stride(0) if M > 1 else max(K, x.stride(0) // 8 * 8)
+    if x.numel() and ((K > 1 and x.stride(1) != 1) or ld < K or ld % 8):
+        raise ValueError("x must hold each row contiguously, rows a multiple of 8 elements apart")
+    return M, K, ld if x.numel() else K
+
+
+def int8_quantize_rows(x, codes=None, scales=None, stream=None):
+    """int8 codes [M, K] and fp32 scales [M] of bf16 x [M, K], a scale per row (``wan_int8_quantize_rows``):
+    an activation's 8-bit checkpoint, or a weight [N, K] with a scale per output channel."""
+    import torch
+    M, K, ldx = _check_activations(x)
+    codes = torch.empty((M, K), dtype=torch.int8, device=x.device) if codes is None else codes
+    scales = torch.empty(M, dtype=torch.float32, device=x.device) if scales is None else scales
+    _check_plain("codes", codes, torch.int8, M * K)
+    _check_plain("scales", scales, torch.float32, M)
+    _check_device(x=x, codes=codes, scales=scales)
+    _check("wan_int8_quantize_rows", lib().wan_int8_quantize_rows(x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                                                  M, K, ldx, _stream_ptr(stream)))
+    return codes, scales
+
+
+def int8_dequantize_rows(codes, scales, x=None, stream=None):
+    """bf16 [M, K] = codes * scales: an 8-bit checkpoint read back (``wan_int8_dequantize_rows``)."""
+    import torch
+    M, K = _check_matrix("codes", codes, torch.int8)
+    _check_plain("scales", scales, torch.float32, M)
+    x = torch.empty((M, K), dtype=torch.bfloat16, device=codes.device) if x is None else x
+    _check_plain("x", x, torch.bfloat16, M * K)
+    _check_device(codes=codes, scales=scales, x=x)
+    _check("wan_int8_dequantize_rows", lib().wan_int8_dequantize_rows(codes.data_ptr(), scales.data_ptr(),
+                                                                      x.data_ptr(), M, K, _stream_ptr(stream)))
+    return x
+
+
+def _check_weight(w_codes, w_scales, bias, K):
+    import torch
+    N, _ = _check_matrix("w_codes", w_codes, torch.int8, K)
+    _check_plain("w_scales", w_scales, torch.float32, N)
+    if bias is not None:
+        _check_plain("bias", bias, torch.bfloat16, N)
+    return N
+
+
+def int8_gemm(a_codes, a_scales, w_codes, w_scales, bias=None, y=None, stream=None):
+    """bf16 Y [M, N] = diag(a_scales) (a_codes w_codes^T) diag(w_scales) + bias through ``wan_int8_gemm``."""
+    import torch
+    M, K = _check_matrix("a_codes", a_codes, torch.int8)
+    _check_plain("a_scales", a_scales, torch.float32, M)
+    N = _check_weight(w_codes, w_scales, bias, K)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=a_codes.device) if y is None else y
+    _check_plain("y", y, torch.bfloat16, M * N)
+    _check_device(a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales, bias=bias, y=y)
+    _check("wan_int8_gemm", lib().wan_int8_gemm(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(),
+                                                w_scales.data_ptr(), None if bias is None else bias.data_ptr(),
+                                                y.data_ptr(), M, N, K, _stream_ptr(stream)))
+    return y
+
+
+def int8_linear(x, w_codes, w_scales, bias=None, return_checkpoint=False, stream=None):
+    """Y = the int8 linear layer of bf16 x [M, K] (rows may be strided) with a weight quantised by
+    int8_quantize_rows (``wan_int8_linear``).  With return_checkpoint: (Y, codes, scales), the 8-bit
+    codes of x that int8_grad_weight takes in the backward."""
+    import torch
+    M, K, ldx = _check_activations(x)
+    N = _check_weight(w_codes, w_scales, bias, K)
+    codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    scales = torch.empty(M, dtype=torch.float32, device=x.device)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    _check_device(x=x, w_codes=w_codes, w_scales=w_scales, bias=bias)
+    _check("wan_int8_linear", lib().wan_int8_linear(x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+                                                    None if bias is None else bias.data_ptr(), y.data_ptr(),
+                                                    codes.data_ptr(), scales.data_ptr(), M, N, K, ldx,
+                                                    _stream_ptr(stream)))
+    return (y, codes, scales) if return_checkpoint else y
+
+
+def int8_grad_weight(dy, codes, scales, dw=None, stream=None):
+    """bf16 dW [N, K] = dY^T (codes * scales) from dY [M, N] and the layer input's 8-bit checkpoint
+    (``wan_int8_grad_weight``)."""
+    import torch
+    M, N = _check_matrix("dy", dy, torch.bfloat16)
+    _, K = _check_matrix("codes", codes, torch.int8)
+    if codes.shape[0] != M:
+        raise ValueError(f"codes has {codes.shape[0]} rows, dy {M}")
+    _check_plain("scales", scales, torch.float32, M)
+    dw = torch.empty((N, K), dtype=torch.bfloat16, device=dy.device) if dw is None else dw
+    _check_plain("dw", dw, torch.bfloat16, N * K)
+    _check_device(dy=dy, codes=codes, scales=scales, dw=dw)
+    _check("wan_int8_grad_weight", lib().wan_int8_grad_weight(dy.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                                              dw.data_ptr(), M, N, K, _stream_ptr(stream)))
+    return dw
+
+
+def int8_grad_input(dy, w_codes, w_scales, dx=None, stream=None):
+    """bf16 dX [M, K] = dY (w_codes * w_scales) from dY [M, N] and the weight's 8-bit codes
+    (``wan_int8_grad_input``)."""
+    import torch
+    M, N = _check_matrix("dy", dy, torch.bfloat16)
+    rows, K = _check_matrix("w_codes", w_codes, torch.int8)
+    if rows != N:
+        raise ValueError(f"w_codes has {rows} rows, dy {N} columns")
+    _check_plain("w_scales", w_scales, torch.float32, N)
+    dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device) if dx is None else dx
+    _check_plain("dx", dx, torch.bfloat16, M * K)
+    _check_device(dy=dy, w_codes=w_codes, w_scales=w_scales, dx=dx)
+    _check("wan_int8_grad_input", lib().wan_int8_grad_input(dy.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+                                                            dx.data_ptr(), M, N, K, _stream_ptr(stream)))
+    return dx
 
 
 def fwd_q8_workspace_size(B, S, H, D=128) -> int:
