@@ -364,6 +364,20 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* o, const v
                : WAN_ATTN_ERR_CUDA;
 }
 
+// Tensor map over a bf16 [T, H, 128] tensor of token stride ld (elements) as 3-D (128, H, T), box
+// (64 of D, `heads`, `tokens`) with the 128-byte swizzle: rows of the tile are token-major.
+bool make_packed_map(CUtensorMap* m, const void* base, int T, int H, long long ld, int heads, int tokens) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {128, (cuuint64_t)H, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {256, (cuuint64_t)ld * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Shape, stride, alignment and overlap checks of the packed attention calls.  A tensor without
 // rows may have a null pointer.
 struct Packed {
@@ -699,7 +713,11 @@ int wan_fp8_gemm(const void* a_codes, const float* a_scales, const void* b_codes
 
 size_t wan_attn_varlen_fwd_workspace_size(int N, int Tq, int Tk, int H, int Hkv, int D) {
     if (check_packed(N, Tq, Tk, H, Hkv, D) != WAN_ATTN_OK) return 0;
-    return 0;
+    int pack, splits;
+    varlen_fwd_plan(N, Tq, Tk, H, Hkv, &pack, &splits);
+    if (splits == 1) return 0;
+    const size_t rows = size_t(splits) * Tq * H;
+    return align256(rows * 128 * 4) + align256(rows * 4);
 }
 
 int wan_attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float* lse, const int* cu_q,
@@ -713,14 +731,34 @@ int wan_attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, fl
     const Packed t[] = {{q, Tq, ldq, H, false}, {k, Tk, ldk, Hkv, false}, {v, Tk, ldv, Hkv, false},
                         {o, Tq, static_cast<long long>(H) * 128, H, true}};
     const Range ins[] = {range_of(cu_q, size_t(N + 1) * 4), range_of(cu_k, size_t(N + 1) * 4)};
-    const Range outs[] = {range_of(lse, size_t(H) * Tq * 4)};
-    st = check_packed_tensors(t, 4, ins, 2, outs, 1);
+    const size_t need = wan_attn_varlen_fwd_workspace_size(N, Tq, Tk, H, Hkv, D);
+    if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return WAN_ATTN_ERR_WORKSPACE;
+    const Range outs[] = {range_of(lse, size_t(H) * Tq * 4), range_of(workspace, need)};
+    st = check_packed_tensors(t, 4, ins, 2, outs, need ? 2 : 1);
     if (st != WAN_ATTN_OK) return st;
     VarlenFwdParams p{};
     if (!fill_packed(p, q, k, v, cu_q, cu_k, N, Tq, Tk, H, Hkv, ldq, ldk, ldv, causal)) return WAN_ATTN_ERR_CUDA;
     p.o = o;
     p.lse = lse;
-    return as_status(launch_varlen_fwd(p, static_cast<cudaStream_t>(stream)));
+    varlen_fwd_plan(N, Tq, Tk, H, Hkv, &p.pack, &p.splits);
+    if (need) {
+        p.o_part = static_cast<float*>(workspace);
+        p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                              align256(size_t(p.splits) * Tq * H * 128 * 4));
+    }
+    CUtensorMap tq, tk, tv, to;
+    if (!make_packed_map(&tq, q, Tq, H, ldq, p.pack, 128 / p.pack) ||
+        !make_packed_map(&to, o, Tq, H, static_cast<long long>(H) * 128, p.pack, 128 / p.pack))
+        return WAN_ATTN_ERR_CUDA;
+    if (Tk > 0) {
+        if (!make_packed_map(&tk, k, Tk, Hkv, ldk, 1, 128) || !make_packed_map(&tv, v, Tk, Hkv, ldv, 1, 128))
+            return WAN_ATTN_ERR_CUDA;
+    } else {
+        tk = tq;                          // never read: without keys no tile has a key block
+        tv = tq;
+    }
+    return as_status(launch_varlen_fwd(tq, tk, tv, to, p, static_cast<cudaStream_t>(stream)));
 }
 
 size_t wan_attn_varlen_bwd_workspace_size(int N, int Tq, int Tk, int H, int Hkv, int D) {

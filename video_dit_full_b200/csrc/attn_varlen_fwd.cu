@@ -1,56 +1,460 @@
-// Packed attention forward: one warp per (query row, head), four dims per lane.
+// Packed attention forward on sm_100a: sequences of different lengths on one token axis, full or
+// causal, grouped heads.
+//
+// For query row i of a sequence with Lq queries and Lk keys (causal: keys j <= i + Lk - Lq)
+//     m = max_j s_ij,  l = sum_j 2^(s_ij - m),  o_i = sum_j 2^(s_ij - m) v_j / l,  lse_i = (m + log2 l) ln 2,
+// s = q.k log2(e) / sqrt(D), in one pass over the keys with a running m and l (fp32).
+//
+// How.  A CTA holds two Q tiles of 128 rows of one sequence and one packed head: a row is a (token,
+// query head of the group) pair, `pack` heads to a token, so that heads that read the same keys share
+// one walk over them (a single token's group is one tile; without packing its keys would cross the
+// memory system once a head).  Then, as the dense forward:
+//   warp 8      TMA producer: the Q tiles, then K_j / V_j of 128 keys into rings of two stages
+//   warp 9      tcgen05 issuer: S_t = Q_t K_j^T (TMEM, fp32), O_t += P_t V_j (P_t in TMEM, bf16)
+//   warps 0-3 / 4-7   softmax of tile 0 / 1, one row per thread; epilogue
+// What packing sequences adds:
+//   - the CTA finds its tile by a scan over the offsets (tile_at): no table, no extra launch
+//   - each tile has its own last key block (causal), blocks behind the diagonal are never loaded, and
+//     only blocks on the diagonal or at the sequence's end are masked (a count per row)
+//   - the last key block may hold the next sequence's rows: its K only meets masked scores, its V rows
+//     are zeroed in shared memory before the tensor core reads them (0 x NaN is NaN)
+//   - a tile that the sequence does not fill is stored row by row; the rows behind it are not touched
+//   - few query rows against many keys: gridDim.z CTAs split the keys and a second kernel joins their
+//     normalised fp32 partial results by their lse
+#include <cuda.h>
+
 #include "sm100_ptx.cuh"
 #include "varlen.cuh"
 
 namespace wan {
 namespace varlen {
 
-__device__ __forceinline__ float4 ld4(const void* base, long long elem) {
-    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + elem);
-    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
+constexpr int BM = 128;        // rows per Q tile
+constexpr int BN = 128;        // keys per K/V tile
+constexpr int HD = 128;        // head dimension
+constexpr int TILE_BYTES = BM * HD * 2;
+constexpr int HALF_BYTES = TILE_BYTES / 2;    // 64 columns of d (one 128-byte swizzle span)
+
+constexpr int OFF_Q = 0;
+constexpr int OFF_K = OFF_Q + 2 * TILE_BYTES;
+constexpr int OFF_V = OFF_K + 2 * TILE_BYTES;
+constexpr int OFF_BAR = OFF_V + 2 * TILE_BYTES;
+enum Bar { Q_FULL = 0, K_FULL = 2, K_EMPTY = 4, V_FULL = 6, V_EMPTY = 8, S_FULL = 10, P_FULL = 12,
+           O_FINAL = 14, V_TAIL = 16, DRAIN = 17, NBARS = 18 };
+constexpr int OFF_TMEM_SLOT = OFF_BAR + NBARS * 8;
+constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
+constexpr int SMEM_BYTES = OFF_ABORT + 8 + 1024;   // slack for 1024-byte alignment of the tiles
+constexpr int NTHREADS = 320;
+constexpr uint32_t TMEM_COLS = 512;            // S0 S1 O0 O1, 128 columns each
+constexpr float RESCALE_THRESHOLD = 8.0f;      // log2 units: keep a stale max while p <= 2^8
+
+__global__ void __launch_bounds__(NTHREADS, 1)
+varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                  const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
+                  const VarlenFwdParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw_addr);
+
+    const int warp = warp_id();
+    const int lane = lane_id();
+    const int pack = p.pack, tile_tokens = BM / pack;
+    const int h0 = blockIdx.y * pack;                 // first query head of the packed group
+    const int hk = h0 / (p.H / p.Hkv);
+
+    // this CTA's place; a sequence's tiles run backwards, so that causal's longest start first
+    const TileAt at = tile_at(p.cu_q, p.N, p.Tq, 2 * tile_tokens, blockIdx.x);
+    if (at.seq < 0) return;                           // the grid is an upper bound
+    const Span sq = span_of(p.cu_q, at.seq, p.Tq), sk = span_of(p.cu_k, at.seq, p.Tk);
+    const int i0 = (at.tiles - 1 - at.tile) * 2 * tile_tokens;      // first token, within the sequence
+    const int nq = i0 + tile_tokens < sq.len ? 2 : 1;
+    const int shift = sk.len - sq.len;                // causal: token i sees keys 0 .. i + shift
+    // key blocks that tile t needs (its last token sees the most), and this split's share of them
+    int nblk[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int last = min(i0 + (t + 1) * tile_tokens, sq.len) - 1;
+        const int keys = t >= nq ? 0 : p.causal ? min(max(last + shift + 1, 0), sk.len) : sk.len;
+        nblk[t] = (keys + BN - 1) / BN;
+    }
+    const int all = max(nblk[0], nblk[1]);
+    const int share = (all + p.splits - 1) / p.splits;
+    const int j0 = min(static_cast<int>(blockIdx.z) * share, all);
+    const int n = min(share, all - j0);               // blocks j0 .. j0 + n - 1
+    int nt[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) nt[t] = min(max(nblk[t] - j0, 0), n);
+
+    const uint32_t sQ = base + OFF_Q, sK = base + OFF_K, sV = base + OFF_V;
+    const uint32_t bar0 = base + OFF_BAR;
+    auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
+    const WaitCtl wc{abort_flag, p.wait_budget_ns, p.status};
+
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(bar(Q_FULL + t), 1);
+            mbar_init(bar(K_FULL + t), 1);
+            mbar_init(bar(K_EMPTY + t), 1);
+            mbar_init(bar(V_FULL + t), 1);
+            mbar_init(bar(V_EMPTY + t), 1);
+            mbar_init(bar(S_FULL + t), 1);
+            mbar_init(bar(P_FULL + t), BM);
+            mbar_init(bar(O_FINAL + t), 1);
+        }
+        mbar_init(bar(V_TAIL), 1);
+        mbar_init(bar(DRAIN), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(base + OFF_TMEM_SLOT, TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
+
+    if (warp == 8) {
+        // ------------------------------ TMA producer ------------------------------
+        // rows of the last block that lie behind the sequence (only the last block of the last split)
+        const int tail = (j0 + n) * BN - sk.len;
+        const int whole = n - (tail > 0 && n > 0 ? 1 : 0);
+        int kpar[2] = {-1, -1}, vpar[2] = {-1, -1};   // parity of the last copy issued per stage
+        bool ok = true;
+        if (lane == 0 && n > 0) {
+            tma_prefetch_desc(&tmk);
+            tma_prefetch_desc(&tmv);
+            const uint64_t keep = l2_policy_evict_last();
+            const uint32_t qbytes = static_cast<uint32_t>(pack * tile_tokens) * 256u;
+            for (int t = 0; t < nq; ++t) {
+                const int tok = sq.begin + i0 + t * tile_tokens;
+                mbar_arrive_expect_tx(bar(Q_FULL + t), qbytes);
+                tma_load_3d(sQ + t * TILE_BYTES, &tmq, bar(Q_FULL + t), 0, h0, tok);
+                tma_load_3d(sQ + t * TILE_BYTES + HALF_BYTES, &tmq, bar(Q_FULL + t), 64, h0, tok);
+            }
+            for (int i = 0; i < n; ++i) {
+                const int s = i & 1;
+                const int use = (i >> 1) & 1;
+                const int tok = sk.begin + (j0 + i) * BN;
+                ok = wait_thread(bar(K_EMPTY + s), use ^ 1, wc);
+                if (!ok) break;
+                mbar_arrive_expect_tx(bar(K_FULL + s), TILE_BYTES);
+                tma_load_3d_hint(sK + s * TILE_BYTES, &tmk, bar(K_FULL + s), 0, hk, tok, keep);
+                tma_load_3d_hint(sK + s * TILE_BYTES + HALF_BYTES, &tmk, bar(K_FULL + s), 64, hk, tok, keep);
+                kpar[s] = use;
+                ok = wait_thread(bar(V_EMPTY + s), use ^ 1, wc);
+                if (!ok) break;
+                const uint32_t full = bar(i < whole ? V_FULL + s : V_TAIL);
+                mbar_arrive_expect_tx(full, TILE_BYTES);
+                tma_load_3d_hint(sV + s * TILE_BYTES, &tmv, full, 0, hk, tok, keep);
+                tma_load_3d_hint(sV + s * TILE_BYTES + HALF_BYTES, &tmv, full, 64, hk, tok, keep);
+                if (i < whole) vpar[s] = use;
+            }
+            if (!ok) {
+                // let the copies already issued land before the CTA's shared memory goes away
+                for (int t = 0; t < nq; ++t) drain_wait(bar(Q_FULL + t), 0);
+                for (int s = 0; s < 2; ++s) {
+                    if (kpar[s] >= 0) drain_wait(bar(K_FULL + s), kpar[s]);
+                    if (vpar[s] >= 0) drain_wait(bar(V_FULL + s), vpar[s]);
+                }
+            }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (ok && whole < n) {
+            // the whole warp zeroes the V rows behind the sequence, then hands the stage over
+            const int s = (n - 1) & 1;
+            if (wait_warp(bar(V_TAIL), 0, wc)) {
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t row0 = sV + s * TILE_BYTES + half * HALF_BYTES + (BN - tail) * 128;
+                    for (int c = lane; c < tail * 8; c += 32) st_shared_v4(row0 + c * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(V_FULL + s));
+            } else {
+                drain_wait(bar(V_TAIL), 0);
+            }
+        }
+    } else if (warp == 9) {
+        // ------------------------------ MMA issuer --------------------------------
+        if (lane == 0 && n > 0) {
+            const uint32_t idesc_qk = make_idesc(1, 1, 1, 0, 0, BM, BN);
+            const uint32_t idesc_pv = make_idesc(1, 1, 1, 0, 1, BM, HD);
+            const uint32_t hi = sdesc_hi();
+            const uint32_t q_lo = sdesc_lo(sQ, 16), k_lo = sdesc_lo(sK, 16), v_lo = sdesc_lo(sV, HALF_BYTES);
+            constexpr uint32_t TILE16 = TILE_BYTES >> 4;
+            auto issue_qk = [&](int t_, int s_) {
+                mma8_f16_ss<HALF_BYTES / 16, 2>(tmem + t_ * BN, q_lo + t_ * TILE16, k_lo + s_ * TILE16, hi, idesc_qk, 0u);
+            };
+            auto issue_pv = [&](int t_, int s_, bool acc) {
+                mma8_f16_ts<32, 512, 128>(tmem + 256 + t_ * HD, tmem + t_ * BN, v_lo + s_ * TILE16, hi, idesc_pv,
+                                          acc ? 1u : 0u);
+            };
+            bool ok = true;
+            for (int t = 0; t < nq && ok; ++t) ok = wait_thread(bar(Q_FULL + t), 0, wc);
+            if (ok) ok = wait_thread(bar(K_FULL + 0), 0, wc);
+            if (ok) {
+                tc_fence_after();
+                for (int t = 0; t < nq; ++t)
+                    if (nt[t] > 0) {
+                        issue_qk(t, 0);
+                        mma_commit(bar(S_FULL + t));
+                    }
+                mma_commit(bar(K_EMPTY + 0));
+            }
+            for (int i = 0; i < n && ok; ++i) {
+                const int s = i & 1;
+                const int s1 = (i + 1) & 1;
+                ok = wait_thread(bar(V_FULL + s), (i >> 1) & 1, wc);
+                bool k_here = false;
+                for (int t = 0; t < nq && ok; ++t) {
+                    if (i >= nt[t]) continue;
+                    ok = wait_thread(bar(P_FULL + t), i & 1, wc);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv(t, s, i > 0);
+                    if (i + 1 == nt[t]) {
+                        mma_commit(bar(O_FINAL + t));
+                    } else {
+                        if (!k_here) {
+                            ok = wait_thread(bar(K_FULL + s1), ((i + 1) >> 1) & 1, wc);
+                            if (!ok) break;
+                            tc_fence_after();
+                            k_here = true;
+                        }
+                        issue_qk(t, s1);
+                        mma_commit(bar(S_FULL + t));
+                    }
+                }
+                if (!ok) break;
+                mma_commit(bar(V_EMPTY + s));
+                if (i + 1 < n) mma_commit(bar(K_EMPTY + s1));
+            }
+            // every MMA issued so far completes before TMEM is released
+            mma_commit(bar(DRAIN));
+            drain_wait(bar(DRAIN), 0);
+        }
+    } else if ((warp >> 2) < nq) {
+        // ------------------------- softmax / correction / epilogue ----------------
+        const int t = warp >> 2;                 // Q tile of this warpgroup
+        const int r = threadIdx.x & 127;         // row within the tile = TMEM lane
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + t * BN + lane_off;
+        const uint32_t tO = tmem + 256 + t * HD + lane_off;
+        const int row_tok = r / pack;
+        const int i_tok = i0 + t * tile_tokens + row_tok;             // token within the sequence
+        const bool real = row_tok < tile_tokens && i_tok < sq.len;
+        const int keys = !real ? 0 : p.causal ? min(max(i_tok + shift + 1, 0), sk.len) : sk.len;
+        const float c = p.scale_log2;
+        float m_ref = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int i = 0; i < nt[t] && ok; ++i) {
+            ok = wait_warp(bar(S_FULL + t), i & 1, wc);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t sr[128];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[q * 32]));
+            tmem_wait_ld();
+            float* s = reinterpret_cast<float*>(sr);
+            const int valid = keys - (j0 + i) * BN;       // keys of this block that the row sees
+            if (__any_sync(0xffffffffu, valid < BN)) {
+#pragma unroll
+                for (int q = 0; q < 128; ++q)
+                    if (q >= valid) s[q] = -INFINITY;
+            }
+            // row max: 8 chains of three-input maxima, then a short tree
+            float m8[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m8[q] = fmax3(s[q], s[q + 8], s[q + 16]);
+#pragma unroll
+            for (int q = 24; q < 128; q += 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    m8[e] = (q + 8 + e < 128) ? fmax3(m8[e], s[q + e], s[q + 8 + e]) : fmaxf(m8[e], s[q + e]);
+            const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+            const float m_cand = mx * c;
+            float alpha = 1.f;
+            bool moved = false;
+            if (m_cand > m_ref + RESCALE_THRESHOLD) {
+                alpha = ex2_approx(m_ref - m_cand);
+                m_ref = m_cand;
+                moved = true;
+            }
+            // P = 2^(s c - m) in packed pairs, the row sum in four independent packed accumulators;
+            // a row that has seen no key yet keeps m = -inf: its scores are all -inf, its P zero
+            const float off = m_ref == -INFINITY ? 0.f : -m_ref;
+            const float2 c2 = make_float2(c, c), n2 = make_float2(off, off);
+            float2 acc[4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) acc[a] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                    const float2 x = ffma2(make_float2(s[half * 64 + 2 * q], s[half * 64 + 2 * q + 1]), c2, n2);
+                    const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                    acc[q & 3] = fadd2(acc[q & 3], e);
+                    pk[q] = pack_bf16x2(e.x, e.y);
+                }
+                tmem_st32(tS + half * 32, pk);
+            }
+            const float2 acc2 = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+            l = l * alpha + (acc2.x + acc2.y);
+            if (i > 0 && __any_sync(0xffffffffu, moved)) {
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + q * 32, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                    tmem_st32(tO + q * 32, o);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(P_FULL + t));
+        }
+        if (ok && nt[t] > 0) ok = wait_warp(bar(O_FINAL + t), 0, wc);
+        // A whole tile leaves through its Q buffer (every MMA that read it has completed) and two TMA
+        // stores; a tile that the sequence does not fill, or a split's partial result, row by row.
+        const bool empty = m_ref == -INFINITY;            // the row saw no key here
+        const float inv_l = empty ? 0.f : 1.f / l;
+        const float lse2 = empty ? -INFINITY : m_ref + log2f(l);
+        const int token = sq.begin + i_tok, head = h0 + r % pack;
+        const bool by_tma = p.splits == 1 && i0 + (t + 1) * tile_tokens <= sq.len && nt[t] > 0;
+        const uint32_t stage = sQ + t * TILE_BYTES;
+        if (ok) {
+            tc_fence_after();
+            const long long row = static_cast<long long>(token) * p.H + head;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {                 // 32 columns of d at a time
+                uint32_t o[32];
+                if (nt[t] > 0) {
+                    tmem_ld32(tO + q * 32, o);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = empty ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv_l);
+                if (p.splits > 1) {
+                    if (real && !empty) {
+                        uint4* dst = reinterpret_cast<uint4*>(
+                            p.o_part + (static_cast<long long>(blockIdx.z) * p.Tq * p.H + row) * HD + q * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                } else {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                    if (by_tma) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            st_shared_v4(sw128_chunk(stage + (q >> 1) * HALF_BYTES, r, (q & 1) * 4 + e), w[4 * e], w[4 * e + 1],
+                                         w[4 * e + 2], w[4 * e + 3]);
+                    } else if (real) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + row * HD + q * 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            if (real) {
+                const long long at_lse = static_cast<long long>(head) * p.Tq + token;
+                if (p.splits > 1) p.lse_part[static_cast<long long>(blockIdx.z) * p.H * p.Tq + at_lse] = lse2;
+                else p.lse[at_lse] = lse2 * 0.69314718055994531f;
+            }
+        }
+        named_bar_sync(1 + t, BM);                // every warp of the group, whatever its state
+        if (r == 0 && ok && by_tma && !*abort_flag) {
+            const int tok = sq.begin + i0 + t * tile_tokens;
+            tma_store_3d(&tmo, stage, 0, h0, tok);
+            tma_store_3d(&tmo, stage + HALF_BYTES, 64, h0, tok);
+            bulk_commit_group();
+            bulk_wait_read_all();                 // the buffer stays valid until the copies have read it
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem, TMEM_COLS);
 }
 
-__global__ void __launch_bounds__(128) varlen_fwd_kernel(const VarlenFwdParams p) {
-    const long long id = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (id >= static_cast<long long>(p.Tq) * p.H) return;
-    const int lane = threadIdx.x & 31, t = static_cast<int>(id / p.H), h = static_cast<int>(id % p.H);
-    const int n = sequence_of(p.cu_q, p.N, t);
-    if (n < 0) return;
-    const Span sq = span_of(p.cu_q, n, p.Tq), sk = span_of(p.cu_k, n, p.Tk);
-    const int hk = h / (p.H / p.Hkv);
-    const int seen = p.causal ? min(sk.len, max(0, t - sq.begin + sk.len - sq.len + 1)) : sk.len;
-    const float4 q = ld4(p.q, t * p.ldq + h * 128 + lane * 4);
-    float m = -INFINITY, l = 0.f;
+// o = sum_z 2^(lse_z - lse) o_z, lse = log2 sum_z 2^lse_z over the splits' partial results: one warp per
+// (token, head) row.  The partial results are few (only calls with few query rows are split).
+__global__ void __launch_bounds__(128) varlen_join_kernel(const VarlenFwdParams p) {
+    const long long rows = static_cast<long long>(p.Tq) * p.H;
+    const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int lane = threadIdx.x & 31, token = static_cast<int>(row / p.H), head = static_cast<int>(row % p.H);
+    if (sequence_of(p.cu_q, p.N, token) < 0) return;
+    const float* lse = p.lse_part + static_cast<long long>(head) * p.Tq + token;
+    float m = -INFINITY;
+    for (int z = 0; z < p.splits; ++z) m = fmaxf(m, lse[z * rows]);
+    float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < seen; ++j) {
-        const long long row = sk.begin + j;
-        const float4 k = ld4(p.k, row * p.ldk + hk * 128 + lane * 4);
-        float s = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s), alpha = ex2_approx(m - mn), e = ex2_approx(s - mn);
-        const float4 v = ld4(p.v, row * p.ldv + hk * 128 + lane * 4);
-        acc = make_float4(acc.x * alpha + e * v.x, acc.y * alpha + e * v.y, acc.z * alpha + e * v.z,
-                          acc.w * alpha + e * v.w);
-        l = l * alpha + e;
-        m = mn;
+    for (int z = 0; z < p.splits; ++z) {
+        const float lz = lse[z * rows];
+        if (lz == -INFINITY) continue;                // nothing was written there
+        const float w = ex2_approx(lz - m);
+        const float4 o = *reinterpret_cast<const float4*>(p.o_part + (z * rows + row) * HD + lane * 4);
+        l += w;
+        acc = make_float4(fmaf(w, o.x, acc.x), fmaf(w, o.y, acc.y), fmaf(w, o.z, acc.z), fmaf(w, o.w, acc.w));
     }
-    const float inv = seen ? 1.f / l : 0.f;
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (static_cast<long long>(t) * p.H + h) * 128 + lane * 4) =
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * HD + lane * 4) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (lane == 0)
-        p.lse[static_cast<long long>(h) * p.Tq + t] = seen ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        p.lse[static_cast<long long>(head) * p.Tq + token] =
+            l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// CTAs along the tile axis, an upper bound from the sizes alone: every sequence wastes less than one tile.
+static long long tile_bound(int N, int Tq, int pack) {
+    const int per_cta = 2 * (BM / pack);
+    const long long bound = static_cast<long long>(Tq) / per_cta + N;
+    return bound < Tq ? bound : Tq;
 }
 
 }  // namespace varlen
 
-int launch_varlen_fwd(const VarlenFwdParams& p, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(p.Tq) * p.H;
-    varlen::varlen_fwd_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+// pack: the most heads of a group that fill at least 120 of a tile's 128 rows (128 / pack tokens of
+// `pack` heads each).  splits: when the tiles alone do not fill the GPU, as many CTAs as give it two
+// waves, of 4 key blocks at least on average.
+void varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv, int* pack, int* splits) {
+    const int group = H / Hkv;
+    int pk = 1;
+    for (int d = 1; d <= group && d <= varlen::BM; ++d)
+        if (group % d == 0 && (varlen::BM / d) * d >= 120) pk = d;
+    *pack = pk;
+    const long long ctas = varlen::tile_bound(N, Tq, pk) * (H / pk);
+    const long long blocks = (static_cast<long long>(Tk) / N + varlen::BN - 1) / varlen::BN;
+    long long s = ctas > 0 && ctas < 2 * 148 ? (2 * 148 + ctas - 1) / ctas : 1;
+    if (s > blocks / 4) s = blocks / 4;
+    if (s > 64) s = 64;
+    *splits = s < 1 ? 1 : static_cast<int>(s);
+}
+
+int launch_varlen_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
+                      const VarlenFwdParams& p, cudaStream_t stream) {
+    if (configure_smem(reinterpret_cast<const void*>(varlen::varlen_fwd_kernel), varlen::SMEM_BYTES) != 0) return -1;
+    const dim3 grid(static_cast<unsigned>(varlen::tile_bound(p.N, p.Tq, p.pack)), p.H / p.pack, p.splits);
+    varlen::varlen_fwd_kernel<<<grid, varlen::NTHREADS, varlen::SMEM_BYTES, stream>>>(tq, tk, tv, to, p);
+    if (cudaGetLastError() != cudaSuccess) return -1;
+    if (p.splits > 1) {
+        const long long rows = static_cast<long long>(p.Tq) * p.H;
+        varlen::varlen_join_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p);
+        if (cudaGetLastError() != cudaSuccess) return -1;
+    }
+    return 0;
 }
 
 }  // namespace wan

@@ -26,5 +26,34 @@ __device__ __forceinline__ int sequence_of(const int* cu, int N, int t) {
     return (lo >= 1 && lo <= N) ? lo - 1 : -1;
 }
 
+// Tile `target` of the tiles that all sequences' rows (on the axis of `cu`) split into, `rows` to a
+// tile and each sequence starting a tile of its own: the sequence and the tile within it, or seq = -1
+// past the last.  The whole warp calls it; 32 sequences a step, so no table has to be built (and no
+// extra launch made) before the attention kernel.
+struct TileAt {
+    int seq, tile, tiles;          // tiles: of that sequence
+};
+__device__ __forceinline__ TileAt tile_at(const int* cu, int N, int T, int rows, int target) {
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (int n0 = 0; n0 < N; n0 += 32) {
+        const int mine = n0 + lane < N ? (span_of(cu, n0 + lane, T).len + rows - 1) / rows : 0;
+        int upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += o;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + upto > target);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            const int tiles = __shfl_sync(0xffffffffu, mine, l);
+            return {n0 + l, target - before - __shfl_sync(0xffffffffu, upto, l) + tiles, tiles};
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return {-1, 0, 0};
+}
+
 }  // namespace varlen
 }  // namespace wan

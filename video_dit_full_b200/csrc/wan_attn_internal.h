@@ -85,6 +85,10 @@ struct VarlenParams {
 struct VarlenFwdParams : VarlenParams {
     void* o;                          // bf16 [Tq, H, 128]
     float* lse;                       // fp32 [H, Tq]
+    int pack;                         // query heads that share a Q tile (a divisor of H / Hkv)
+    int splits;                       // CTAs among which a tile's keys are split
+    float* o_part;                    // workspace fp32 [splits, Tq, H, 128], splits > 1 only
+    float* lse_part;                  // workspace fp32 [splits, H, Tq] (base-2 log)
 };
 struct VarlenBwdParams : VarlenParams {
     const void *o, *dout;             // bf16 [Tq, H, 128]
@@ -132,7 +136,11 @@ int launch_fp8_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensor
                     cudaStream_t stream);
 
 // Packed attention (attn_varlen_fwd.cu, attn_varlen_bwd.cu).  0 on success.
-int launch_varlen_fwd(const VarlenFwdParams& p, cudaStream_t stream);
+// tq, to: maps over q and o (128, H, Tq) with boxes (64, pack, 128 / pack); tk, tv: (128, Hkv, Tk), (64, 1, 128).
+int launch_varlen_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
+                      const VarlenFwdParams& p, cudaStream_t stream);
+// How the forward lays out a call: heads per Q tile and splits of the keys (see VarlenFwdParams).
+void varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv, int* pack, int* splits);
 int launch_varlen_bwd(const VarlenBwdParams& p, cudaStream_t stream);
 
 // Int8 linear layer (int8_linear.cu) and its backward (int8_grad.cu).  0 on success.
