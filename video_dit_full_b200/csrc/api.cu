@@ -378,6 +378,20 @@ bool make_packed_map(CUtensorMap* m, const void* base, int T, int H, long long l
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tensor map over an fp32 accumulator [T, H, 128] as 3-D (128, H, T), box (`cols`, 1, 128); `swizzle`:
+// the 128-byte swizzle (cols = 32).
+bool make_packed_acc_map(CUtensorMap* m, void* base, int T, int H, int cols, bool swizzle) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {128, (cuuint64_t)H, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {128 * 4, (cuuint64_t)H * 128 * 4};
+    const cuuint32_t box[3] = {(cuuint32_t)cols, 1, 128};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Shape, stride, alignment and overlap checks of the packed attention calls.  A tensor without
 // rows may have a null pointer.
 struct Packed {
@@ -755,15 +769,16 @@ int wan_attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, fl
         if (!make_packed_map(&tk, k, Tk, Hkv, ldk, 1, 128) || !make_packed_map(&tv, v, Tk, Hkv, ldv, 1, 128))
             return WAN_ATTN_ERR_CUDA;
     } else {
-        tk = tq;                          // never read: without keys no tile has a key block
-        tv = tq;
+        tk = tv = tq;                     // never read: without keys no tile has a key block
     }
     return as_status(launch_varlen_fwd(tq, tk, tv, to, p, static_cast<cudaStream_t>(stream)));
 }
 
 size_t wan_attn_varlen_bwd_workspace_size(int N, int Tq, int Tk, int H, int Hkv, int D) {
     if (check_packed(N, Tq, Tk, H, Hkv, D) != WAN_ATTN_OK) return 0;
-    return 256;
+    size_t bytes = align256(size_t(Tq) * H * 128 * 4) + align256(size_t(Tq) * H * 4);
+    if (varlen_bwd_splits(N, Tq, Tk, H, Hkv) > 1) bytes += 2 * align256(size_t(Tk) * Hkv * 128 * 4);
+    return bytes;
 }
 
 int wan_attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o, const void* dO, const float* lse,
@@ -776,7 +791,7 @@ int wan_attn_varlen_bwd(const void* q, const void* k, const void* v, const void*
     if (Tq == 0 && Tk == 0) return WAN_ATTN_OK;
     if (Tq > 0 && (!lse || !aligned16(lse))) return WAN_ATTN_ERR_INVALID_ARG;
     const size_t need = wan_attn_varlen_bwd_workspace_size(N, Tq, Tk, H, Hkv, D);
-    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
         return WAN_ATTN_ERR_WORKSPACE;
     const long long hd = static_cast<long long>(H) * 128;
     const Packed t[] = {{q, Tq, ldq, H, false},  {k, Tk, ldk, Hkv, false},  {v, Tk, ldv, Hkv, false},
@@ -798,7 +813,25 @@ int wan_attn_varlen_bwd(const void* q, const void* k, const void* v, const void*
     p.lddq = lddq;
     p.lddk = lddk;
     p.lddv = lddv;
-    return as_status(launch_varlen_bwd(p, static_cast<cudaStream_t>(stream)));
+    p.splits = varlen_bwd_splits(N, Tq, Tk, H, Hkv);
+    char* ws = static_cast<char*>(workspace);
+    const size_t off_delta = align256(size_t(Tq) * H * 128 * 4), off_dk = off_delta + align256(size_t(Tq) * H * 4);
+    p.dq_acc = reinterpret_cast<float*>(ws);
+    p.delta = reinterpret_cast<float*>(ws + off_delta);
+    if (p.splits > 1) {
+        p.dk_acc = reinterpret_cast<float*>(ws + off_dk);
+        p.dv_acc = reinterpret_cast<float*>(ws + off_dk + align256(size_t(Tk) * Hkv * 128 * 4));
+    }
+    CUtensorMap tq{}, tk{}, tv{}, tdo{}, tdq{}, tdk{}, tdv{};        // those of an empty axis are never read
+    if (Tq > 0 && (!make_packed_map(&tq, q, Tq, H, ldq, 1, 128) || !make_packed_map(&tdo, dO, Tq, H, hd, 1, 128) ||
+                   !make_packed_acc_map(&tdq, p.dq_acc, Tq, H, 128, false)))
+        return WAN_ATTN_ERR_CUDA;
+    if (Tk > 0 && (!make_packed_map(&tk, k, Tk, Hkv, ldk, 1, 128) || !make_packed_map(&tv, v, Tk, Hkv, ldv, 1, 128)))
+        return WAN_ATTN_ERR_CUDA;
+    if (p.splits > 1 && (!make_packed_acc_map(&tdk, p.dk_acc, Tk, Hkv, 32, true) ||
+                         !make_packed_acc_map(&tdv, p.dv_acc, Tk, Hkv, 32, true)))
+        return WAN_ATTN_ERR_CUDA;
+    return as_status(launch_varlen_bwd(tq, tk, tv, tdo, tdq, tdk, tdv, p, static_cast<cudaStream_t>(stream)));
 }
 
 int wan_int8_quantize_rows(const void* x, void* codes, float* scales, int M, int K, int64_t ldx, void* stream) {

@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(128) varlen_join_kernel(const VarlenFwdParams 
     const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     if (row >= rows) return;
     const int lane = threadIdx.x & 31, token = static_cast<int>(row / p.H), head = static_cast<int>(row % p.H);
-    if (sequence_of(p.cu_q, p.N, token) < 0) return;
+    if (token < p.cu_q[0] || token >= p.cu_q[p.N]) return;       // outside every sequence
     const float* lse = p.lse_part + static_cast<long long>(head) * p.Tq + token;
     float m = -INFINITY;
     for (int z = 0; z < p.splits; ++z) m = fmaxf(m, lse[z * rows]);

@@ -15,17 +15,6 @@ __device__ __forceinline__ Span span_of(const int* cu, int n, int T) {
     return {a, max(b - a, 0)};
 }
 
-// The sequence that owns token t: the last n with cu[n] <= t, if t < cu[n + 1]; else -1.
-__device__ __forceinline__ int sequence_of(const int* cu, int N, int t) {
-    int lo = 0, hi = N + 1;                     // cu[lo - 1] <= t < cu[hi] (with cu[-1] = -inf, cu[N + 1] = inf)
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= t) lo = mid + 1;
-        else hi = mid;
-    }
-    return (lo >= 1 && lo <= N) ? lo - 1 : -1;
-}
-
 // Tile `target` of the tiles that all sequences' rows (on the axis of `cu`) split into, `rows` to a
 // tile and each sequence starting a tile of its own: the sequence and the tile within it, or seq = -1
 // past the last.  The whole warp calls it; 32 sequences a step, so no table has to be built (and no

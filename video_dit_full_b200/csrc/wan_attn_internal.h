@@ -95,6 +95,10 @@ struct VarlenBwdParams : VarlenParams {
     const float* lse;                 // fp32 [H, Tq]
     void *dq, *dk, *dv;               // bf16, token strides below
     long long lddq, lddk, lddv;
+    int splits;                       // CTAs sharing one key tile, each over its own run of Q tiles
+    float* dq_acc;                    // workspace fp32 [Tq, H, 128]: unscaled dS K
+    float* delta;                     // workspace fp32 [H, Tq]: rowsum(dO * O)
+    float *dk_acc, *dv_acc;           // workspace fp32 [Tk, Hkv, 128], splits > 1 only
 };
 
 // Device address of the status word on the current device (nullptr on failure).
@@ -141,7 +145,12 @@ int launch_varlen_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
                       const VarlenFwdParams& p, cudaStream_t stream);
 // How the forward lays out a call: heads per Q tile and splits of the keys (see VarlenFwdParams).
 void varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv, int* pack, int* splits);
-int launch_varlen_bwd(const VarlenBwdParams& p, cudaStream_t stream);
+// tq, tk, tv, tdo: boxes (64, 1, 128); tdq: fp32 [Tq, H, 128], box (128, 1, 128); tdk, tdv: fp32
+// [Tk, Hkv, 128], boxes (32, 1, 128) with the 128-byte swizzle, only read when p.splits > 1.
+int launch_varlen_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
+                      const CUtensorMap& tdq, const CUtensorMap& tdk, const CUtensorMap& tdv, const VarlenBwdParams& p,
+                      cudaStream_t stream);
+int varlen_bwd_splits(int N, int Tq, int Tk, int H, int Hkv);
 
 // Int8 linear layer (int8_linear.cu) and its backward (int8_grad.cu).  0 on success.
 int launch_int8_quant_rows(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream);
