@@ -501,6 +501,28 @@ int check_args(const Arg* a, int n) {
     return WAN_ATTN_OK;
 }
 
+// The int8 product on validated arguments.
+int int8_product(const void* a_codes, const float* a_scales, const void* b_codes, const float* b_scales,
+                 const void* bias, void* y, int M, int N, int K, bool after_quant, cudaStream_t stream) {
+    Int8GemmParams p;
+    p.a_scales = a_scales;
+    p.b_scales = b_scales;
+    p.bias = static_cast<const __nv_bfloat16*>(bias);
+    p.y = static_cast<__nv_bfloat16*>(y);
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.after_quant = after_quant ? 1 : 0;
+    p.wait_budget_ns = wait_budget_ns();
+    p.status = device_status_word();
+    if (!p.status) return WAN_ATTN_ERR_CUDA;
+    const int tokens = int8_gemm_token_tile(M, N);
+    CUtensorMap tx, tw;
+    if (!make_rows_u8_map(&tx, a_codes, M, K, tokens ? tokens : 128) || !make_rows_u8_map(&tw, b_codes, N, K, 128))
+        return WAN_ATTN_ERR_CUDA;
+    return launch_int8_gemm(tx, tw, p, stream) == 0 ? WAN_ATTN_OK : WAN_ATTN_ERR_CUDA;
+}
+
 int as_status(int rc) { return rc == 0 ? WAN_ATTN_OK : WAN_ATTN_ERR_CUDA; }
 
 }  // namespace
@@ -865,8 +887,7 @@ int wan_int8_gemm(const void* a_codes, const float* a_scales, const void* b_code
                      {y, size_t(M) * N * 2, 15, true},    {bias, size_t(N) * 2, 15, false}};
     const int sa = check_args(a, bias ? 6 : 5);
     if (sa != WAN_ATTN_OK) return sa;
-    return as_status(launch_int8_gemm(a_codes, a_scales, b_codes, b_scales, bias, y, M, N, K,
-                                      static_cast<cudaStream_t>(stream)));
+    return int8_product(a_codes, a_scales, b_codes, b_scales, bias, y, M, N, K, false, static_cast<cudaStream_t>(stream));
 }
 
 int wan_int8_linear(const void* x, const void* w_codes, const float* w_scales, const void* bias, void* y, void* codes,
@@ -882,7 +903,7 @@ int wan_int8_linear(const void* x, const void* w_codes, const float* w_scales, c
     if (sa != WAN_ATTN_OK) return sa;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (launch_int8_quant_rows(x, codes, scales, M, K, ldx, s) != 0) return WAN_ATTN_ERR_CUDA;
-    return as_status(launch_int8_gemm(codes, scales, w_codes, w_scales, bias, y, M, N, K, s));
+    return int8_product(codes, scales, w_codes, w_scales, bias, y, M, N, K, true, s);
 }
 
 int wan_int8_grad_weight(const void* dy, const void* codes, const float* scales, void* dw, int M, int N, int K,

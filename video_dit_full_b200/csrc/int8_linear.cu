@@ -1,87 +1,582 @@
-// Int8 linear layer: row quantiser, its inverse, and Y = diag(sx) (Cx Cw^T) diag(sw) + bias.
+// Int8 linear layer on sm_100a: rows to 8 bits and back, and Y = diag(sx) (Cx Cw^T) diag(sw) + bias.
+//
+//   quant_rows     s = absmax / 127, c = rint(127 x / absmax) per row
+//   dequant_rows   x = bf16(s c)
+//   gemm_pair      many tokens: CTA pairs (tcgen05 cta_group::2), 256 x 256 tiles, kind::i8 into int32 TMEM
+//   gemm_few       few tokens: the weight's 128 channels are the MMA's M, 16 to 128 tokens its N; a cluster
+//                  splits K and adds its exact int32 partial sums through distributed shared memory
+// Sums are exact in int32 (K <= 131072), so neither the tiling nor the split changes a result.
+#include <cuda.h>
+
 #include "sm100_ptx.cuh"
 #include "wan_attn_internal.h"
 
 namespace wan {
 namespace int8 {
 
-// One warp per row.  Codes are rint of the exact quotient 127 x / absmax: 127 x is exact in fp32
-// (7 + 8 bits) and the division is correctly rounded; a quotient that is not a half-integer is at
-// least 2^-9 away from one (its denominator has 8 bits), far more than the rounding error.
+// ------------------------------------------------------------------------------------
+// rows <-> 8 bits
+// ------------------------------------------------------------------------------------
+constexpr int CACHED = 4;          // 8-element pieces of a row that a thread keeps between its two passes
+
+__device__ __forceinline__ float2 bf16x2_floats(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// rint of the exact quotient 127 x / amax, half to even, as the low byte of the result.  127 x is exact in
+// fp32 (7 + 8 bits).  q = 127 x * inv is within an ulp of the quotient, the fma's residual 127 x - q amax is
+// exact, and one correction gives the correctly rounded quotient (Markstein's division, inv = RN(1 / amax)).
+// A quotient of these 8-bit significands that is not a half-integer is at least 2^-9 away from one, so
+// rounding it again to an integer is rounding the exact quotient; a half-integer is represented exactly.
+__device__ __forceinline__ uint32_t code_of(float x, float amax, float inv) {
+    const float a = 127.f * x;
+    const float q = a * inv;
+    const float r = fmaf(fmaf(-q, amax, a), inv, q);
+    return __float_as_uint(r + 12582912.f);                // 1.5 * 2^23: the sum's low bits are the integer
+}
+__device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, float pre, float amax, float inv) {
+    const float2 a = bf16x2_floats(lo), b = bf16x2_floats(hi);
+    const uint32_t c0 = code_of(a.x * pre, amax, inv), c1 = code_of(a.y * pre, amax, inv);
+    const uint32_t c2 = code_of(b.x * pre, amax, inv), c3 = code_of(b.y * pre, amax, inv);
+    return __byte_perm(__byte_perm(c0, c1, 0x0040), __byte_perm(c2, c3, 0x0040), 0x5410);
+}
+
+// T threads per row (a power of two, 32 to 256), 256 / T rows per block.  Bound by memory: x is read once
+// (rows of up to 32 T elements stay in registers between the absmax and the codes), the codes written once.
+template <int T>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16* __restrict__ x, int8_t* __restrict__ codes,
                                                          float* __restrict__ scales, int M, int K, long long ldx) {
-    const int lane = threadIdx.x & 31;
-    const long long m = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (m >= M) return;
-    float amax = 0.f;
-    bool bad = false;
-    for (int k = lane; k < K; k += 32) {
-        const float f = fabsf(__bfloat162float(x[m * ldx + k]));
-        bad |= !(f <= 3.4e38f);
-        amax = fmaxf(amax, f);
-    }
+    grid_launch_dependents();                              // a layer's product may fetch its weight meanwhile
+    __shared__ uint32_t top[8];
+    const int tid = threadIdx.x % T;
+    const long long m = static_cast<long long>(blockIdx.x) * (256 / T) + threadIdx.x / T;
+    const bool here = m < M;
+    const uint4* row = reinterpret_cast<const uint4*>(x + (here ? m : 0) * ldx);
+    const int pieces = here ? K / 8 : 0;
+    uint4 kept[CACHED];
+    // |x| as bits: the largest finite magnitude orders like an integer, and an infinity or NaN above it
+    uint32_t amax_bits = 0;
+    auto fold = [&](uint4 u) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0) scales[m] = bad ? NAN : amax > 0.f ? __fdiv_rn(amax, 127.f) : 1.f;
-    const float pre = amax > 1e30f ? 0x1p-32f : 1.f;          // 127 x must not overflow; exact, as the powers of two are
-    for (int k = lane; k < K; k += 32)
-        codes[m * K + k] = (bad || !(amax > 0.f)) ? 0
-                               : static_cast<int8_t>(__float2int_rn(
-                                     __fdiv_rn(127.f * (pre * __bfloat162float(x[m * ldx + k])), pre * amax)));
+        for (int e = 0; e < 4; ++e) amax_bits = max(amax_bits, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+    };
+#pragma unroll
+    for (int c = 0; c < CACHED; ++c)
+        if (c * T + tid < pieces) kept[c] = row[c * T + tid];
+#pragma unroll
+    for (int c = 0; c < CACHED; ++c)
+        if (c * T + tid < pieces) fold(kept[c]);
+    for (int c = CACHED * T + tid; c < pieces; c += T) fold(row[c]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) amax_bits = max(amax_bits, __shfl_xor_sync(0xffffffffu, amax_bits, off));
+    if (T > 32) {
+        if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = amax_bits;
+        __syncthreads();
+        const int first = (threadIdx.x / T) * (T / 32);
+#pragma unroll
+        for (int w = 0; w < T / 32; ++w) amax_bits = max(amax_bits, top[first + w]);
+    }
+    const bool bad = amax_bits >= 0x7f80u, zero = amax_bits == 0;
+    float amax = __uint_as_float(amax_bits << 16);
+    if (here && tid == 0) scales[m] = bad ? __uint_as_float(0x7fc00000u) : zero ? 1.f : __fdiv_rn(amax, 127.f);
+    // powers of two keep 127 x and 1 / amax inside fp32's range, and change no quotient
+    const float pre = bad || zero ? 0.f : amax < 0x1p-100f ? 0x1p100f : amax > 0x1p100f ? 0x1p-100f : 1.f;
+    amax = bad || zero ? 1.f : amax * pre;
+    const float inv = __frcp_rn(amax);
+    uint2* out = reinterpret_cast<uint2*>(codes + (here ? m : 0) * K);
+    auto put = [&](int c, uint4 u) {
+        if (bad) u = make_uint4(0u, 0u, 0u, 0u);           // 0 * inf is not 0
+        out[c] = make_uint2(codes4(u.x, u.y, pre, amax, inv), codes4(u.z, u.w, pre, amax, inv));
+    };
+#pragma unroll
+    for (int c = 0; c < CACHED; ++c)
+        if (c * T + tid < pieces) put(c * T + tid, kept[c]);
+    for (int c = CACHED * T + tid; c < pieces; c += T) put(c, row[c]);
 }
 
-__global__ void __launch_bounds__(256) dequant_rows_kernel(const int8_t* __restrict__ codes, const float* __restrict__ scales,
-                                                           __nv_bfloat16* __restrict__ x, int K, long long n) {
-    for (long long t = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; t < n; t += 256ll * gridDim.x)
-        x[t] = __float2bfloat16_rn(scales[t / K] * codes[t]);
+// 16 codes per thread and step; K % 16 == 0, so they are of one row.  Bound by memory.
+__global__ void __launch_bounds__(256) dequant_rows_kernel(const uint4* __restrict__ codes, const float* __restrict__ scales,
+                                                           uint4* __restrict__ x, int K16, long long n16) {
+    for (long long t = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; t < n16; t += 256ll * gridDim.x) {
+        const uint4 u = codes[t];
+        const float s = scales[t / K16];
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int a = static_cast<int>(w[e]);
+            o[2 * e] = pack_bf16x2(s * static_cast<float>(a << 24 >> 24), s * static_cast<float>(a << 16 >> 24));
+            o[2 * e + 1] = pack_bf16x2(s * static_cast<float>(a << 8 >> 24), s * static_cast<float>(a >> 24));
+        }
+        x[2 * t] = make_uint4(o[0], o[1], o[2], o[3]);
+        x[2 * t + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
 }
 
-__global__ void __launch_bounds__(256) gemm_kernel(const int8_t* __restrict__ a, const float* __restrict__ sa,
-                                                   const int8_t* __restrict__ b, const float* __restrict__ sb,
-                                                   const __nv_bfloat16* __restrict__ bias, __nv_bfloat16* __restrict__ y,
-                                                   int M, int N, int K) {
-    __shared__ int as[16][17], bs[16][17];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const long long m = blockIdx.x * 16ll + ty;
-    const int n = blockIdx.y * 16 + tx, nb = blockIdx.y * 16 + ty;
-    int acc = 0;
-    for (int k = 0; k < K; k += 64) {
-        const int kk = k + tx * 4;
-        as[ty][tx] = (m < M && kk < K) ? *reinterpret_cast<const int*>(a + m * K + kk) : 0;
-        bs[ty][tx] = (nb < N && kk < K) ? *reinterpret_cast<const int*>(b + static_cast<long long>(nb) * K + kk) : 0;
-        __syncthreads();
+// ------------------------------------------------------------------------------------
+// product
+// ------------------------------------------------------------------------------------
+constexpr int BK = 128;                              // bytes = codes of K per stage
+constexpr int NTHREADS = 192;                        // warp 0 TMA, 1 MMA, 2-5 epilogue
+
+// y = acc * (sx * sw) + bias.  int32 -> fp32 rounds at 2^-24, far below the bf16 result's 2^-8.
+__device__ __forceinline__ float result(uint32_t acc, float sx, float sw, float bias) {
+    return fmaf(static_cast<float>(static_cast<int>(acc)), sx * sw, bias);
+}
+
+__device__ __forceinline__ void mma_i8_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Many tokens.  Persistent CTA pairs walk 256 x 256 output tiles; CTA r of a pair loads rows 128 r.. of the
+// tile's tokens and of its channels (half of each operand), the leader issues M256 N256 K32 MMAs that read
+// both CTAs' shared memory, and each CTA's TMEM holds its own 128 rows of two accumulators in turn, so that
+// the epilogue of one tile runs under the next one's products.  Tiles go in groups of 16 row blocks with the
+// row block fastest: the tiles in flight share a few blocks of each operand in L2.
+namespace pair {
+constexpr int BN = 256, STAGES = 6, GROUP_M = 16;
+constexpr int HALF_BYTES = 128 * BK, STAGE_BYTES = 2 * HALF_BYTES;       // A rows | B half rows
+constexpr int OFF_BAR = STAGES * STAGE_BYTES;
+enum Bar { FULL = 0, EMPTY = STAGES, TFULL = 2 * STAGES, TEMPTY = 2 * STAGES + 2, DRAIN = 2 * STAGES + 4,
+           NBARS = 2 * STAGES + 5 };
+constexpr int OFF_TMEM_SLOT = OFF_BAR + NBARS * 8;
+constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
+constexpr int OFF_EPI = (OFF_ABORT + 8 + 15) & ~15;                      // per epilogue warp: 32 rows x 64 B
+constexpr int EPI_WARP_BYTES = 32 * 64;
+constexpr int SMEM_BYTES = OFF_EPI + 4 * EPI_WARP_BYTES + 1024;
+constexpr uint32_t TMEM_COLS = 512;                                      // two 256-column int32 accumulators
+
+__device__ __forceinline__ void tile_of(long long t, int m_tiles, int n_tiles, int& mb, int& nb) {
+    const long long per_group = static_cast<long long>(GROUP_M) * n_tiles;
+    const int g = static_cast<int>(t / per_group);
+    const int rows = min(GROUP_M, m_tiles - g * GROUP_M);
+    const long long w = t - g * per_group;
+    mb = g * GROUP_M + static_cast<int>(w % rows);
+    nb = static_cast<int>(w / rows);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
+gemm_pair_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
+                 const Int8GemmParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;     // the same offset in both CTAs
+    uint8_t* smem = smem_raw + (base - raw_addr);
+    const int warp = warp_id(), lane = lane_id();
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const uint32_t bar0 = base + OFF_BAR;
+    auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
+    const WaitCtl wc{abort_flag, p.wait_budget_ns, p.status};
+
+    const int m_tiles = (p.M + 255) / 256, n_tiles = (p.N + BN - 1) / BN;
+    const long long tiles = static_cast<long long>(m_tiles) * n_tiles;
+    const int nk = (p.K + BK - 1) / BK;
+    const long long pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar(FULL + s), 1);
+            mbar_init(bar(EMPTY + s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(TFULL + b), 1);
+            mbar_init(bar(TEMPTY + b), 256);
+        }
+        mbar_init(bar(DRAIN), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + OFF_TMEM_SLOT),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync_all();                 // both CTAs' barriers and TMEM exist before any remote use
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
+
+    if (warp == 0) {
+        // ---------------- TMA producer (both CTAs; bytes counted on the leader's FULL) ----------------
+        if (lane == 0) {
+            tma_prefetch_desc(&tma_a);
+            tma_prefetch_desc(&tma_b);
+            int par[STAGES];
+            for (int s = 0; s < STAGES; ++s) par[s] = -1;
+            long long it = 0;
+            bool ok = true;
+            for (long long t = pair; t < tiles && ok; t += npairs) {
+                int mb, nbk;
+                tile_of(t, m_tiles, n_tiles, mb, nbk);
+                const int m0 = mb * 256 + static_cast<int>(rank) * 128;
+                const int nb = nbk * BN + static_cast<int>(rank) * 128;
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const int s = static_cast<int>(it % STAGES);
+                    const int use = static_cast<int>((it / STAGES) & 1);
+                    ok = wait_thread(bar(EMPTY + s), use ^ 1, wc);
+                    if (!ok) break;
+                    if (leader) mbar_arrive_expect_tx(bar(FULL + s), 2 * STAGE_BYTES);
+                    const uint32_t full = mapa_shared(bar(FULL + s), 0);
+                    const uint32_t st = base + s * STAGE_BYTES;
+                    tma_load_2d_pair(st, &tma_a, full, kb * BK, m0);
+                    tma_load_2d_pair(st + HALF_BYTES, &tma_b, full, kb * BK, nb);
+                    par[s] = use;
+                }
+            }
+            if (!ok && leader)
+                for (int s = 0; s < STAGES; ++s)
+                    if (par[s] >= 0) drain_wait(bar(FULL + s), par[s]);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (leader only) ----------------
+        if (lane == 0 && leader) {
+            const uint32_t idesc = make_idesc(2, 1, 1, 0, 0, 256, BN);       // s32 <- s8 x s8, K-major
+            long long it = 0;
+            int tc = 0;
+            bool ok = true;
+            for (long long t = pair; t < tiles && ok; t += npairs, ++tc) {
+                const int b = tc & 1;
+                ok = wait_thread(bar(TEMPTY + b), ((tc >> 1) & 1) ^ 1, wc);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + b * BN;
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const int s = static_cast<int>(it % STAGES);
+                    ok = wait_thread(bar(FULL + s), static_cast<int>((it / STAGES) & 1), wc);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sa = base + s * STAGE_BYTES, sb = sa + HALF_BYTES;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc = __dp4a(as[ty][e], bs[tx][e], acc);
-        __syncthreads();
+                    for (int kk = 0; kk < BK / 32; ++kk)
+                        mma_i8_ss_pair(acc, sdesc_sw128(sa + kk * 32, 16, 1024), sdesc_sw128(sb + kk * 32, 16, 1024),
+                                       idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit_pair(bar(EMPTY + s));                         // both CTAs' stage s is free
+                    mma_commit_pair(mapa_shared(bar(EMPTY + s), 1));
+                }
+                if (!ok) break;
+                mma_commit_pair(bar(TFULL + b));
+                mma_commit_pair(mapa_shared(bar(TFULL + b), 1));
+            }
+            mma_commit_pair(bar(DRAIN));
+            drain_wait(bar(DRAIN), 0);
+        }
+    } else {
+        // ---------------- epilogue (both CTAs: each its own 128 rows) ----------------
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tempty_leader = mapa_shared(bar(TEMPTY), 0);
+        int tc = 0;
+        bool ok = true;
+        for (long long t = pair; t < tiles && ok; t += npairs, ++tc) {
+            int mb, nbk;
+            tile_of(t, m_tiles, n_tiles, mb, nbk);
+            const int m0 = mb * 256 + static_cast<int>(rank) * 128;
+            const int n0 = nbk * BN;
+            const int b = tc & 1;
+            ok = wait_warp(bar(TFULL + b), (tc >> 1) & 1, wc);
+            if (!ok) break;
+            tc_fence_after();
+            const int m = m0 + r;
+            const float sx = m < p.M ? p.a_scales[m] : 0.f;
+            // each 32-column chunk goes through the warp's 2 KB of shared memory (16-byte pieces
+            // swizzled by row / 2), so that a store writes 8 whole 64-byte row segments
+            uint8_t* wbuf = smem + OFF_EPI + (warp - 2) * EPI_WARP_BYTES;
+            const int row0 = m0 + (warp & 3) * 32;                           // this warp's 32 rows
+#pragma unroll 1
+            for (int c = 0; c < BN / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld32(tmem + b * BN + lane_off + c * 32, v);
+                tmem_wait_ld();
+                if (n0 + c * 32 >= p.N) continue;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    // 8 channels (N % 8 == 0: all there or none); the same addresses in every lane
+                    const int n = n0 + c * 32 + q * 8;
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (n < p.N) {
+                        float sw[8], bi[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) sw[e] = p.b_scales[n + e];
+                        const uint4 u = p.bias ? *reinterpret_cast<const uint4*>(p.bias + n) : w;
+                        const uint32_t bw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = bf16x2_floats(bw[e]);
+                            bi[2 * e] = f.x;
+                            bi[2 * e + 1] = f.y;
+                        }
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = pack_bf16x2(result(v[q * 8 + 2 * e], sx, sw[2 * e], bi[2 * e]),
+                                               result(v[q * 8 + 2 * e + 1], sx, sw[2 * e + 1], bi[2 * e + 1]));
+                        w = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    *reinterpret_cast<uint4*>(wbuf + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16)) = w;
+                }
+                __syncwarp();
+                const int n = n0 + c * 32 + (lane & 3) * 8;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int rr = 8 * k + (lane >> 2);
+                    const uint4 val =
+                        *reinterpret_cast<const uint4*>(wbuf + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) * 16));
+                    const int mm = row0 + rr;
+                    if (mm < p.M && n < p.N)
+                        *reinterpret_cast<uint4*>(p.y + static_cast<long long>(mm) * p.N + n) = val;
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            mbar_arrive_cluster(tempty_leader + 8u * static_cast<uint32_t>(b));   // leader's TEMPTY[b]
+        }
     }
-    if (m < M && n < N) {
-        const float f = static_cast<float>(acc) * (sa[m] * sb[n]) + (bias ? __bfloat162float(bias[n]) : 0.f);
-        y[m * N + n] = __float2bfloat16_rn(f);
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();                 // no CTA leaves while its peer may still signal it
+    tc_fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS)
+                                : "memory");
+}
+}  // namespace pair
+
+// Few tokens: bound by reading the weight once.  The MMA's M is 128 channels, its N is NT tokens (the tile
+// that a row of tokens would leave mostly empty the other way round).  The CTAs of a cluster share a tile
+// and split K, so that a layer of a few dozen channel tiles still keeps every SM loading; each keeps its
+// int32 partial tile in shared memory, and after a cluster barrier every CTA adds up (exactly) and stores
+// its share of the tokens.  Launched behind the quantiser as a dependent launch it fetches its first
+// weight stages while the quantiser still runs (p.after_quant).
+namespace few {
+template <int NT>
+struct Cfg {
+    static constexpr int A_BYTES = 128 * BK, B_BYTES = NT * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = NT <= 32 ? 5 : NT == 64 ? 4 : 3;           // two CTAs per SM
+    static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
+    static constexpr int FULL = 0, EMPTY = STAGES, DONE = 2 * STAGES, NBARS = 2 * STAGES + 1;
+    static constexpr int OFF_TMEM_SLOT = OFF_BAR + NBARS * 8;
+    static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
+    static constexpr int SMEM_BYTES = OFF_ABORT + 8 + 1024;
+    static constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
+    static_assert(NT * 128 * 4 <= STAGES * STAGE_BYTES, "the partial tile reuses the stages");
+    static_assert(2 * SMEM_BYTES <= 228 * 1024 - 2048, "two CTAs per SM");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(NTHREADS, 2)
+gemm_few_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w,
+                const Int8GemmParams p) {
+    using C = Cfg<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;     // the same offset in every CTA
+    uint8_t* smem = smem_raw + (base - raw_addr);
+    const int warp = warp_id(), lane = lane_id();
+    const int splits = gridDim.x, rank = blockIdx.x;       // the cluster is the grid's x
+    const int n0 = blockIdx.y * 128, m0 = blockIdx.z * NT;
+    const int nk_all = (p.K + BK - 1) / BK;
+    const int k0 = rank * nk_all / splits, nk = (rank + 1) * nk_all / splits - k0;
+    const uint32_t bar0 = base + C::OFF_BAR;
+    auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
+    const WaitCtl wc{abort_flag, p.wait_budget_ns, p.status};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(bar(C::FULL + s), 1);
+            mbar_init(bar(C::EMPTY + s), 1);
+        }
+        mbar_init(bar(C::DONE), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
     }
+    if (warp == 1) {
+        tmem_alloc(base + C::OFF_TMEM_SLOT, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TMEM_SLOT);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tma_x);
+            tma_prefetch_desc(&tma_w);
+            auto load_w = [&](int kb) {
+                const int s = kb % C::STAGES;
+                mbar_arrive_expect_tx(bar(C::FULL + s), C::STAGE_BYTES);
+                tma_load_2d(base + s * C::STAGE_BYTES, &tma_w, bar(C::FULL + s), (k0 + kb) * BK, n0);
+            };
+            auto load_x = [&](int kb) {
+                const int s = kb % C::STAGES;
+                tma_load_2d(base + s * C::STAGE_BYTES + C::A_BYTES, &tma_x, bar(C::FULL + s), (k0 + kb) * BK, m0);
+            };
+            const int early = min(nk, C::STAGES);
+            for (int kb = 0; kb < early; ++kb) load_w(kb);
+            if (p.after_quant) grid_dependency_wait();     // x's codes are the quantiser's
+            for (int kb = 0; kb < early; ++kb) load_x(kb);
+            int issued = early;
+            bool ok = true;
+            for (int kb = early; kb < nk; ++kb) {
+                ok = wait_thread(bar(C::EMPTY + kb % C::STAGES), ((kb / C::STAGES) & 1) ^ 1, wc);
+                if (!ok) break;
+                load_w(kb);
+                load_x(kb);
+                issued = kb + 1;
+            }
+            if (!ok)
+                for (int kb = max(0, issued - C::STAGES); kb < issued; ++kb)
+                    drain_wait(bar(C::FULL + kb % C::STAGES), (kb / C::STAGES) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = make_idesc(2, 1, 1, 0, 0, 128, NT);       // s32 <- s8 x s8, K-major
+            for (int kb = 0; kb < nk; ++kb) {
+                const int s = kb % C::STAGES;
+                if (!wait_thread(bar(C::FULL + s), (kb / C::STAGES) & 1, wc)) break;
+                tc_fence_after();
+                const uint32_t sa = base + s * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+#pragma unroll
+                for (int kk = 0; kk < BK / 32; ++kk)
+                    mma_i8_ss(tmem, sdesc_sw128(sa + kk * 32, 16, 1024), sdesc_sw128(sb + kk * 32, 16, 1024), idesc,
+                              (kb > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(bar(C::EMPTY + s));
+            }
+            mma_commit(bar(C::DONE));                      // all of this CTA's products, also after a time-out
+        }
+    } else {
+        // partial tile [token][channel] (int32) over the stages, which every MMA has read by now
+        const bool ok = wait_warp(bar(C::DONE), 0, wc);
+        if (ok) {
+            tc_fence_after();
+            const int ch = (warp & 3) * 32 + lane;
+            const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            int* part = reinterpret_cast<int*>(smem);
+#pragma unroll 1
+            for (int t = 0; t < NT; t += 16) {
+                uint32_t v[16];
+                tmem_ld16(src + t, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) part[(t + e) * 128 + ch] = static_cast<int>(v[e]);
+            }
+        } else {
+            drain_wait(bar(C::DONE), 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (splits > 1) cluster_sync_all();
+    tc_fence_after();
+
+    // tokens rank, rank + splits, ... of the tile: one warp a token, four channels a lane
+    if (p.after_quant) grid_dependency_wait();             // the scales are the quantiser's
+    const int n = n0 + lane * 4;
+    if (!*abort_flag && n < p.N) {
+        const float4 sw = make_float4(p.b_scales[n], p.b_scales[n + 1], p.b_scales[n + 2], p.b_scales[n + 3]);
+        float2 b01 = make_float2(0.f, 0.f), b23 = b01;
+        if (p.bias) {
+            const uint2 u = *reinterpret_cast<const uint2*>(p.bias + n);
+            b01 = bf16x2_floats(u.x);
+            b23 = bf16x2_floats(u.y);
+        }
+        const int tokens = min(NT, p.M - m0);
+        for (int t = rank + warp * splits; t < tokens; t += (NTHREADS / 32) * splits) {
+            const uint32_t at = base + (t * 128 + lane * 4) * 4;
+            uint4 acc = make_uint4(0u, 0u, 0u, 0u);
+            for (int z = 0; z < splits; ++z) {
+                const uint4 v = ld_shared_cluster_v4(splits > 1 ? mapa_shared(at, z) : at);
+                acc = make_uint4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
+            }
+            const float sx = p.a_scales[m0 + t];
+            *reinterpret_cast<uint2*>(p.y + static_cast<long long>(m0 + t) * p.N + n) =
+                make_uint2(pack_bf16x2(result(acc.x, sx, sw.x, b01.x), result(acc.y, sx, sw.y, b01.y)),
+                           pack_bf16x2(result(acc.z, sx, sw.z, b23.x), result(acc.w, sx, sw.w, b23.y)));
+        }
+    }
+    __syncthreads();
+    if (splits > 1) cluster_sync_all();                    // no CTA leaves while a peer reads its partial tile
+    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+template <int NT>
+int launch(const CUtensorMap& tx, const CUtensorMap& tw, const Int8GemmParams& p, cudaStream_t stream) {
+    if (configure_smem(reinterpret_cast<const void*>(gemm_few_kernel<NT>), Cfg<NT>::SMEM_BYTES) != 0) return -1;
+    const int n_tiles = (p.N + 127) / 128, m_tiles = (p.M + NT - 1) / NT, nk = (p.K + BK - 1) / BK;
+    // K is split while the CTAs stay within two per SM and each has two stages of K or more
+    int splits = 1;
+    while (splits < 8 && 2ll * splits * n_tiles * m_tiles <= 2 * 148 && nk / (2 * splits) >= 2) splits *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(splits, n_tiles, m_tiles);
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = Cfg<NT>::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.after_quant ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, gemm_few_kernel<NT>, tx, tw, p) == cudaSuccess ? 0 : -1;
+}
+}  // namespace few
+
+template <int T>
+void launch_quant(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream) {
+    const int rows = 256 / T;
+    quant_rows_kernel<T><<<(M + rows - 1) / rows, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(x),
+                                                                    static_cast<int8_t*>(codes), scales, M, K, ldx);
 }
 
 }  // namespace int8
 
 int launch_int8_quant_rows(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream) {
-    int8::quant_rows_kernel<<<(M + 7) / 8, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(x),
-                                                             static_cast<int8_t*>(codes), scales, M, K, ldx);
+    if (K <= 1024) int8::launch_quant<32>(x, codes, scales, M, K, ldx, stream);
+    else if (K <= 2048) int8::launch_quant<64>(x, codes, scales, M, K, ldx, stream);
+    else if (K <= 4096) int8::launch_quant<128>(x, codes, scales, M, K, ldx, stream);
+    else int8::launch_quant<256>(x, codes, scales, M, K, ldx, stream);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 int launch_int8_dequant_rows(const void* codes, const float* scales, void* x, int M, int K, cudaStream_t stream) {
-    int8::dequant_rows_kernel<<<148 * 8, 256, 0, stream>>>(static_cast<const int8_t*>(codes), scales,
-                                                           static_cast<__nv_bfloat16*>(x), K, static_cast<long long>(M) * K);
+    const long long n16 = static_cast<long long>(M) * K / 16, blocks = (n16 + 255) / 256;
+    int8::dequant_rows_kernel<<<static_cast<unsigned>(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, stream>>>(
+        static_cast<const uint4*>(codes), scales, static_cast<uint4*>(x), K / 16, n16);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
-int launch_int8_gemm(const void* a_codes, const float* a_scales, const void* b_codes, const float* b_scales,
-                     const void* bias, void* y, int M, int N, int K, cudaStream_t stream) {
-    const dim3 grid((M + 15) / 16, (N + 15) / 16);
-    int8::gemm_kernel<<<grid, 256, 0, stream>>>(static_cast<const int8_t*>(a_codes), a_scales,
-                                                static_cast<const int8_t*>(b_codes), b_scales,
-                                                static_cast<const __nv_bfloat16*>(bias), static_cast<__nv_bfloat16*>(y),
-                                                M, N, K);
+int int8_gemm_token_tile(int M, int N) {
+    // pairs where their 256 x 256 tiles occupy at least half of the SMs (and where the other kernel's
+    // channel tiles would not fit a grid)
+    if ((static_cast<long long>((M + 255) / 256) * ((N + 255) / 256) * 2 >= 74 && M > 128) || N > 65535 * 128) return 0;
+    return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+}
+
+int launch_int8_gemm(const CUtensorMap& tx, const CUtensorMap& tw, const Int8GemmParams& p, cudaStream_t stream) {
+    switch (int8_gemm_token_tile(p.M, p.N)) {
+        case 16: return int8::few::launch<16>(tx, tw, p, stream);
+        case 32: return int8::few::launch<32>(tx, tw, p, stream);
+        case 64: return int8::few::launch<64>(tx, tw, p, stream);
+        case 128: return int8::few::launch<128>(tx, tw, p, stream);
+    }
+    namespace pr = int8::pair;
+    if (configure_smem(reinterpret_cast<const void*>(pr::gemm_pair_kernel), pr::SMEM_BYTES) != 0) return -1;
+    const long long tiles = static_cast<long long>((p.M + 255) / 256) * ((p.N + pr::BN - 1) / pr::BN);
+    const int grid = 2 * static_cast<int>(tiles < 74 ? tiles : 74);
+    pr::gemm_pair_kernel<<<grid, int8::NTHREADS, pr::SMEM_BYTES, stream>>>(tx, tw, p);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 

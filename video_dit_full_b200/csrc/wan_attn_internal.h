@@ -101,6 +101,16 @@ struct VarlenBwdParams : VarlenParams {
     float *dk_acc, *dv_acc;           // workspace fp32 [Tk, Hkv, 128], splits > 1 only
 };
 
+struct Int8GemmParams {
+    const float *a_scales, *b_scales; // fp32 [M], [N]
+    const __nv_bfloat16* bias;        // [N] or null
+    __nv_bfloat16* y;                 // [M, N]
+    int M, N, K;
+    int after_quant;                  // launched as the dependent of the quantiser that writes x's codes and scales
+    unsigned long long wait_budget_ns;
+    int* status;
+};
+
 // Device address of the status word on the current device (nullptr on failure).
 int* device_status_word();
 unsigned long long wait_budget_ns();
@@ -155,8 +165,10 @@ int varlen_bwd_splits(int N, int Tq, int Tk, int H, int Hkv);
 // Int8 linear layer (int8_linear.cu) and its backward (int8_grad.cu).  0 on success.
 int launch_int8_quant_rows(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream);
 int launch_int8_dequant_rows(const void* codes, const float* scales, void* x, int M, int K, cudaStream_t stream);
-int launch_int8_gemm(const void* a_codes, const float* a_scales, const void* b_codes, const float* b_scales,
-                     const void* bias, void* y, int M, int N, int K, cudaStream_t stream);
+// Tokens of one tile of the few-token kernel for this size, or 0 for the CTA-pair kernel.
+int int8_gemm_token_tile(int M, int N);
+// tx: x's codes, boxes of the token tile's rows (128 for pairs); tw: the weight's codes, boxes of 128 rows.
+int launch_int8_gemm(const CUtensorMap& tx, const CUtensorMap& tw, const Int8GemmParams& p, cudaStream_t stream);
 // out[r, c] = sum_t a(t, r) s[t] codes[t, c], a(t, r) = dy[t, r] (a_by_row = 0: dW) or dy[r, t] (1: dX)
 int launch_int8_grad(const void* dy, const void* codes, const float* scales, void* out, int rows, int cols, int terms,
                      int a_by_row, cudaStream_t stream);
