@@ -523,6 +523,30 @@ int int8_product(const void* a_codes, const float* a_scales, const void* b_codes
     return launch_int8_gemm(tx, tw, p, stream) == 0 ? WAN_ATTN_OK : WAN_ATTN_ERR_CUDA;
 }
 
+// The products of the int8 layer's backward on validated arguments (dy bf16 [M, N]; codes [terms, K]).
+int int8_grad_product(const void* dy, const void* codes, const float* scales, void* out, int M, int N, int K, bool weight,
+                      cudaStream_t stream) {
+    auto enc = tensor_map_encoder();
+    int* status = device_status_word();
+    if (!enc || !status) return WAN_ATTN_ERR_CUDA;
+    const int terms = weight ? M : N;
+    CUtensorMap tdy, tcodes;
+    const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M}, strides[1] = {(cuuint64_t)N * 2};
+    const cuuint32_t box[2] = {64, weight ? 64u : 128u}, estr[2] = {1, 1};
+    const cuuint64_t cdims[2] = {(cuuint64_t)K, (cuuint64_t)terms}, cstrides[1] = {(cuuint64_t)K};
+    const cuuint32_t cbox[2] = {128, 64};
+    if (enc(&tdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(dy), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+        enc(&tcodes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), cdims, cstrides, cbox, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return WAN_ATTN_ERR_CUDA;
+    return launch_int8_grad(tdy, tcodes, scales, out, weight ? N : M, K, terms, weight, wait_budget_ns(), status, stream) == 0
+               ? WAN_ATTN_OK
+               : WAN_ATTN_ERR_CUDA;
+}
+
 int as_status(int rc) { return rc == 0 ? WAN_ATTN_OK : WAN_ATTN_ERR_CUDA; }
 
 }  // namespace
@@ -919,7 +943,7 @@ int wan_int8_grad_weight(const void* dy, const void* codes, const float* scales,
                      {scales, size_t(M) * 4, 3, false}, {dw, size_t(N) * K * 2, 15, true}};
     const int sa = check_args(a, 4);
     if (sa != WAN_ATTN_OK) return sa;
-    return as_status(launch_int8_grad(dy, codes, scales, dw, N, K, M, 0, s));
+    return int8_grad_product(dy, codes, scales, dw, M, N, K, true, s);
 }
 
 int wan_int8_grad_input(const void* dy, const void* w_codes, const float* w_scales, void* dx, int M, int N, int K,
@@ -931,7 +955,7 @@ int wan_int8_grad_input(const void* dy, const void* w_codes, const float* w_scal
                      {w_scales, size_t(N) * 4, 3, false}, {dx, size_t(M) * K * 2, 15, true}};
     const int sa = check_args(a, 4);
     if (sa != WAN_ATTN_OK) return sa;
-    return as_status(launch_int8_grad(dy, w_codes, w_scales, dx, M, K, N, 1, static_cast<cudaStream_t>(stream)));
+    return int8_grad_product(dy, w_codes, w_scales, dx, M, N, K, false, static_cast<cudaStream_t>(stream));
 }
 
 int wan_attn_sync_status(void* stream) {

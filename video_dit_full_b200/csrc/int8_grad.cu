@@ -1,40 +1,470 @@
-// The int8 linear layer's backward: out[r, c] = sum_t a(t, r) s[t] codes[t, c] (dW and dX).
+// The int8 linear layer's backward from 8-bit operands on sm_100a:
+//     out[r, c] = sum_t a(t, r) x[t, c],   x[t, c] = s[t] codes[t, c]
+// with a(t, r) = dY[t, r] for dW (t = tokens; the codes are the activation's checkpoint) and
+// a(t, r) = dY[r, t] for dX (t = output channels; the codes are the weight's).
+//
+// Bound by the bf16 tensor cores.  The codes stay 8 bits until they are in shared memory: TMA brings
+// [64 t][128 c] bytes, four converter warps multiply by the row's scale in fp32 and write bf16 into the
+// swizzled layout that the MMA reads, so the dequantised matrix never exists in memory (a pass of its
+// own would write and read 4 bytes for every code).  The one rounding on the way, x to bf16 (2^-8
+// relative at most), is what the tensor core's operand type costs; dY is used as it is, sums are fp32.
+// Byte to float costs one PRMT and half an add: the code + 128 goes under the exponent of 2^23.
+//
+// Two launches of the same roles (warp 0 TMA, 1 MMA, 2-5 epilogue, 6-9 converters; a stage holds A, the
+// codes and their bf16 form, 16 + 8 + 16 KB):
+//   PAIR   persistent CTA pairs (cta_group::2) on 256 x 256 tiles: each CTA converts its 128 columns of
+//          the pair's 256, half of what a CTA alone would have to for the same number of products
+//   else   one 128 x 128 tile per CTA; a cluster splits t and joins its fp32 partial tiles in rank order
+//          (deterministic) through distributed shared memory: sizes whose 256 x 256 tiles leave SMs idle
+#include <cuda.h>
+
 #include "sm100_ptx.cuh"
 #include "wan_attn_internal.h"
 
 namespace wan {
-namespace int8 {
+namespace int8_grad {
 
-__global__ void __launch_bounds__(256) grad_kernel(const __nv_bfloat16* __restrict__ dy, const int8_t* __restrict__ codes,
-                                                   const float* __restrict__ s, __nv_bfloat16* __restrict__ out, int rows,
-                                                   int cols, int terms, int a_by_row) {
-    __shared__ float as[16][17], bs[16][17];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const long long r0 = blockIdx.x * 16ll, c = blockIdx.y * 16ll + tx;
-    float acc = 0.f;
-    for (int t0 = 0; t0 < terms; t0 += 16) {
-        // as[term][row]
-        const long long r = a_by_row ? r0 + ty : r0 + tx, t = a_by_row ? t0 + tx : t0 + ty;
-        const float av = (r < rows && t < terms) ? __bfloat162float(a_by_row ? dy[r * terms + t] : dy[t * rows + r]) : 0.f;
-        if (a_by_row) as[tx][ty] = av;
-        else as[ty][tx] = av;
-        bs[ty][tx] = (t0 + ty < terms && c < cols) ? s[t0 + ty] * codes[static_cast<long long>(t0 + ty) * cols + c] : 0.f;
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc = fmaf(as[e][ty], bs[e][tx], acc);
-        __syncthreads();
-    }
-    if (r0 + ty < rows && c < cols) out[(r0 + ty) * cols + c] = __float2bfloat16_rn(acc);
+constexpr int BT = 64;                                       // terms of the sum per stage
+constexpr int STAGES = 5;
+constexpr int A_BYTES = 128 * BT * 2, C_BYTES = 128 * BT, B_BYTES = 128 * BT * 2;
+constexpr int HALF_BYTES = B_BYTES / 2;                      // 64 columns of an MN-major tile
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES + C_BYTES;     // A | B | codes
+constexpr int OFF_BAR = STAGES * STAGE_BYTES;
+enum Bar { FULL = 0, CODES = STAGES, READY = 2 * STAGES, EMPTY = 3 * STAGES, TFULL = 4 * STAGES, TEMPTY = 4 * STAGES + 2,
+           DRAIN = 4 * STAGES + 4, NBARS = 4 * STAGES + 5 };
+constexpr int OFF_TMEM_SLOT = OFF_BAR + NBARS * 8;
+constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
+constexpr int OFF_EPI = (OFF_ABORT + 8 + 15) & ~15;          // per epilogue warp: 32 rows x 64 B
+constexpr int EPI_WARP_BYTES = 32 * 64;
+constexpr int SMEM_BYTES = OFF_EPI + 4 * EPI_WARP_BYTES + 1024;
+constexpr int NTHREADS = 320;
+constexpr int GROUP = 16;                                    // tile order: row blocks in groups
+static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
+static_assert(128 * 128 * 4 <= STAGES * STAGE_BYTES, "a partial tile reuses the stages");
+
+struct Params {
+    const float* scales;              // fp32 [terms]
+    __nv_bfloat16* out;               // [rows, cols]
+    int rows, cols, terms;
+    unsigned long long wait_budget_ns;
+    int* status;
+};
+
+__device__ __forceinline__ void mma_f16_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
-}  // namespace int8
+// wait_thread with acquire at cluster scope: what the peer CTA wrote before its arrival is visible.
+__device__ __forceinline__ bool wait_thread_cluster(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if (t0 == 0) t0 = global_timer_ns();
+        if ((it & 15u) == 0 && wait_expired(w, t0)) return false;
+    }
+}
 
-int launch_int8_grad(const void* dy, const void* codes, const float* scales, void* out, int rows, int cols, int terms,
-                     int a_by_row, cudaStream_t stream) {
-    const dim3 grid((rows + 15) / 16, (cols + 15) / 16);
-    int8::grad_kernel<<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(dy), static_cast<const int8_t*>(codes),
-                                                scales, static_cast<__nv_bfloat16*>(out), rows, cols, terms, a_by_row);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+// Two codes (bytes of w, biased by 128) times s, as packed bf16.
+template <uint32_t SEL0, uint32_t SEL1>
+__device__ __forceinline__ uint32_t scale2(uint32_t w, float2 s) {
+    const float2 f = make_float2(__uint_as_float(__byte_perm(w, 0x4b000000u, SEL0)),
+                                 __uint_as_float(__byte_perm(w, 0x4b000000u, SEL1)));     // 2^23 + code + 128
+    const float2 c = fadd2(f, make_float2(-8388736.f, -8388736.f));                       // the code, exactly
+    const float2 x = fmul2(c, s);
+    return pack_bf16x2(x.x, x.y);
+}
+
+template <bool A_MN, bool PAIR>
+__device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtensorMap& tma_c, const Params& p) {
+    constexpr int CG = PAIR ? 2 : 1, TILE = 128 * CG;
+    constexpr uint32_t TMEM_COLS = 2 * TILE;                 // two fp32 accumulators
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;       // the same offset in every CTA
+    uint8_t* smem = smem_raw + (base - raw_addr);
+    const int warp = warp_id(), lane = lane_id();
+    const int rank = static_cast<int>(cluster_ctarank());
+    const bool leader = !PAIR || rank == 0;
+    const uint32_t bar0 = base + OFF_BAR;
+    auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
+    const WaitCtl wc{abort_flag, p.wait_budget_ns, p.status};
+
+    const int r_tiles = (p.rows + TILE - 1) / TILE, c_tiles = (p.cols + TILE - 1) / TILE;
+    const long long tiles = static_cast<long long>(r_tiles) * c_tiles;
+    const int nk_all = (p.terms + BT - 1) / BT;
+    // PAIR: tiles first, first + step, ...; else one tile and this rank's share of the terms
+    const int splits = PAIR ? 1 : gridDim.x;
+    const long long first = PAIR ? blockIdx.x >> 1 : static_cast<long long>(blockIdx.y) + 65535ll * blockIdx.z;
+    const long long step = PAIR ? gridDim.x >> 1 : tiles;
+    const int k0 = PAIR ? 0 : static_cast<int>(static_cast<long long>(rank) * nk_all / splits);
+    const int nk = (PAIR ? nk_all : static_cast<int>(static_cast<long long>(rank + 1) * nk_all / splits)) - k0;
+    if (!PAIR && first >= tiles) return;                     // the whole cluster (the grid's y, z may overshoot)
+    // row blocks in groups of GROUP, the row block fastest: tiles in flight share both operands in L2
+    auto tile_of = [&](long long t, int& r0, int& c0) {
+        const long long per_group = static_cast<long long>(GROUP) * c_tiles;
+        const int g = static_cast<int>(t / per_group);
+        const int rows = min(GROUP, r_tiles - g * GROUP);
+        const long long w = t - g * per_group;
+        r0 = (g * GROUP + static_cast<int>(w % rows)) * TILE;
+        c0 = static_cast<int>(w / rows) * TILE;
+        if (PAIR) {                                          // this CTA's rows of A and columns of B
+            r0 += rank * 128;
+            c0 += rank * 128;
+        }
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar(FULL + s), 1);
+            mbar_init(bar(CODES + s), 1);
+            mbar_init(bar(READY + s), 4 * CG);
+            mbar_init(bar(EMPTY + s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(TFULL + b), 1);
+            mbar_init(bar(TEMPTY + b), 128 * CG);
+        }
+        mbar_init(bar(DRAIN), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + OFF_TMEM_SLOT),
+                         "r"(TMEM_COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            tmem_alloc(base + OFF_TMEM_SLOT, TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before();
+    if (PAIR) cluster_sync_all();       // both CTAs' barriers and TMEM exist before any remote use
+    else __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
+
+    if (warp == 0) {
+        // ------------------------------ TMA producer ------------------------------
+        if (lane == 0) {
+            tma_prefetch_desc(&tma_a);
+            tma_prefetch_desc(&tma_c);
+            int par[STAGES];
+            for (int s = 0; s < STAGES; ++s) par[s] = -1;
+            long long it = 0;
+            bool ok = true;
+            for (long long t = first; t < tiles && ok; t += step) {
+                int r0, c0;
+                tile_of(t, r0, c0);
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const int s = static_cast<int>(it % STAGES);
+                    const int use = static_cast<int>((it / STAGES) & 1);
+                    ok = wait_thread(bar(EMPTY + s), use ^ 1, wc);
+                    if (!ok) break;
+                    const uint32_t st = base + s * STAGE_BYTES;
+                    const int t0 = (k0 + kb) * BT;
+                    mbar_arrive_expect_tx(bar(CODES + s), C_BYTES);
+                    tma_load_2d(st + A_BYTES + B_BYTES, &tma_c, bar(CODES + s), c0, t0);
+                    if (leader) mbar_arrive_expect_tx(bar(FULL + s), CG * A_BYTES);
+                    // A: [64 t][2 x 64 r] (dW, MN-major) or [128 r][64 t] (dX, K-major)
+                    if (PAIR) {
+                        const uint32_t full = mapa_shared(bar(FULL + s), 0);
+                        if (A_MN) {
+                            tma_load_2d_pair(st, &tma_a, full, r0, t0);
+                            tma_load_2d_pair(st + HALF_BYTES, &tma_a, full, r0 + 64, t0);
+                        } else {
+                            tma_load_2d_pair(st, &tma_a, full, t0, r0);
+                        }
+                    } else if (A_MN) {
+                        tma_load_2d(st, &tma_a, bar(FULL + s), r0, t0);
+                        tma_load_2d(st + HALF_BYTES, &tma_a, bar(FULL + s), r0 + 64, t0);
+                    } else {
+                        tma_load_2d(st, &tma_a, bar(FULL + s), t0, r0);
+                    }
+                    par[s] = use;
+                }
+            }
+            if (!ok)
+                for (int s = 0; s < STAGES; ++s)
+                    if (par[s] >= 0) {
+                        drain_wait(bar(CODES + s), par[s]);
+                        if (leader) drain_wait(bar(FULL + s), par[s]);
+                    }
+        }
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer (a pair's leader) --------------
+        if (lane == 0 && leader) {
+            const uint32_t idesc = make_idesc(1, 1, 1, A_MN ? 1 : 0, 1, TILE, TILE);
+            long long it = 0;
+            int tc = 0;
+            bool ok = true;
+            for (long long t = first; t < tiles && ok; t += step, ++tc) {
+                const int b = tc & 1;
+                ok = wait_thread(bar(TEMPTY + b), ((tc >> 1) & 1) ^ 1, wc);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + b * TILE;
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const int s = static_cast<int>(it % STAGES);
+                    const uint32_t use = static_cast<uint32_t>((it / STAGES) & 1);
+                    ok = wait_thread(bar(FULL + s), use, wc);
+                    if (ok) ok = PAIR ? wait_thread_cluster(bar(READY + s), use, wc) : wait_thread(bar(READY + s), use, wc);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < BT / 16; ++kk) {
+                        // K-major: 16 terms are 32 bytes of a row; MN-major: 16 rows of 128 bytes, halves
+                        // of the other axis HALF_BYTES apart
+                        const uint64_t a = A_MN ? sdesc_sw128(sa + kk * 2048, HALF_BYTES, 1024) : sdesc_sw128(sa + kk * 32, 16, 1024);
+                        const uint64_t bd = sdesc_sw128(sb + kk * 2048, HALF_BYTES, 1024);
+                        const uint32_t accumulate = (kb > 0 || kk > 0) ? 1u : 0u;
+                        if (PAIR) mma_f16_ss_pair(acc, a, bd, idesc, accumulate);
+                        else mma_f16_ss(acc, a, bd, idesc, accumulate);
+                    }
+                    if (PAIR) {
+                        mma_commit_pair(bar(EMPTY + s));                     // both CTAs' stage s is free
+                        mma_commit_pair(mapa_shared(bar(EMPTY + s), 1));
+                    } else {
+                        mma_commit(bar(EMPTY + s));
+                    }
+                }
+                if (!ok) break;
+                if (PAIR) {
+                    mma_commit_pair(bar(TFULL + b));
+                    mma_commit_pair(mapa_shared(bar(TFULL + b), 1));
+                } else {
+                    mma_commit(bar(TFULL + b));
+                }
+            }
+            if (PAIR) mma_commit_pair(bar(DRAIN));
+            else mma_commit(bar(DRAIN));
+            drain_wait(bar(DRAIN), 0);
+        }
+    } else if (warp >= 6) {
+        // ------------------------------ converters --------------------------------
+        // Warp w of the four takes terms 16w .. 16w + 15 of a stage, four at a time: eight lanes read a
+        // term's 128 codes (16 each) and write them as two 16-byte chunks of its swizzled bf16 row.
+        const int w = warp - 6, sub = lane >> 3, ch = lane & 7;
+        const uint32_t odd = ch >> 2;                        // lanes 4-7 (the other half) write their chunks in
+        const uint32_t ready = PAIR ? mapa_shared(bar(READY), 0) : bar(READY);   // reverse: no bank conflicts
+        float s_next[4];
+        auto load_scales = [&](int kb) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int t = (k0 + kb) * BT + w * 16 + q * 4 + sub;
+                s_next[q] = t < p.terms ? p.scales[t] : 0.f;
+            }
+        };
+        load_scales(0);
+        long long it = 0;
+        bool ok = true;
+        for (long long t = first; t < tiles && ok; t += step)
+            for (int kb = 0; kb < nk; ++kb, ++it) {
+                const int s = static_cast<int>(it % STAGES);
+                float sc[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sc[q] = s_next[q];
+                load_scales(kb + 1 < nk ? kb + 1 : 0);       // the next stage's, behind this one's wait
+                ok = wait_warp(bar(CODES + s), static_cast<uint32_t>((it / STAGES) & 1), wc);
+                if (!ok) break;
+                const uint32_t sb = base + s * STAGE_BYTES + A_BYTES;
+                const uint8_t* src = smem + s * STAGE_BYTES + A_BYTES + B_BYTES;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int row = w * 16 + q * 4 + sub;
+                    const uint4 u = *reinterpret_cast<const uint4*>(src + row * 128 + ch * 16);
+                    const uint32_t x[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
+                    const float2 s2 = make_float2(sc[q], sc[q]);
+                    uint32_t o[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[2 * e] = scale2<0x7540, 0x7541>(x[e], s2);
+                        o[2 * e + 1] = scale2<0x7542, 0x7543>(x[e], s2);
+                    }
+                    const uint32_t half = sb + (ch >> 2) * HALF_BYTES;
+                    const int c0 = (ch & 3) * 2;
+                    const uint32_t a0 = sw128_chunk(half, row, c0), a1 = sw128_chunk(half, row, c0 + 1);
+                    if (odd) {
+                        st_shared_v4(a1, o[4], o[5], o[6], o[7]);
+                        st_shared_v4(a0, o[0], o[1], o[2], o[3]);
+                    } else {
+                        st_shared_v4(a0, o[0], o[1], o[2], o[3]);
+                        st_shared_v4(a1, o[4], o[5], o[6], o[7]);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_cluster(ready + 8u * static_cast<uint32_t>(s));
+                    else mbar_arrive(ready + 8u * static_cast<uint32_t>(s));
+                }
+            }
+    } else if (PAIR || splits == 1) {
+        // ------------------------------ epilogue: this CTA's 128 rows -------------
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tempty = PAIR ? mapa_shared(bar(TEMPTY), 0) : bar(TEMPTY);
+        int tc = 0;
+        bool ok = true;
+        for (long long t = first; t < tiles && ok; t += step, ++tc) {
+            int r0, c0;
+            tile_of(t, r0, c0);
+            if (PAIR) c0 -= rank * 128;                      // the accumulator spans the pair's columns
+            const int b = tc & 1;
+            ok = wait_warp(bar(TFULL + b), (tc >> 1) & 1, wc);
+            if (!ok) break;
+            tc_fence_after();
+            // each 32-column chunk goes through the warp's 2 KB of shared memory (16-byte pieces
+            // swizzled by row / 2), so that a store writes 8 whole 64-byte row segments
+            uint8_t* wbuf = smem + OFF_EPI + (warp - 2) * EPI_WARP_BYTES;
+            const int row0 = r0 + (warp & 3) * 32;
+#pragma unroll 1
+            for (int c = 0; c < TILE / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld32(tmem + b * TILE + lane_off + c * 32, v);
+                tmem_wait_ld();
+                if (c0 + c * 32 >= p.cols) continue;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = pack_bf16x2(__uint_as_float(v[q * 8 + 2 * e]), __uint_as_float(v[q * 8 + 2 * e + 1]));
+                    *reinterpret_cast<uint4*>(wbuf + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                __syncwarp();
+                const int col = c0 + c * 32 + (lane & 3) * 8;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int rr = 8 * k + (lane >> 2);
+                    const uint4 val =
+                        *reinterpret_cast<const uint4*>(wbuf + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) * 16));
+                    if (row0 + rr < p.rows && col < p.cols)  // cols % 16 == 0
+                        *reinterpret_cast<uint4*>(p.out + static_cast<long long>(row0 + rr) * p.cols + col) = val;
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            if (PAIR) mbar_arrive_cluster(tempty + 8u * static_cast<uint32_t>(b));
+            else mbar_arrive(tempty + 8u * static_cast<uint32_t>(b));
+        }
+    } else {
+        // ------------------------------ split: partial tile to shared memory ------
+        // [row][column] fp32 over the stages (every copy has landed and every MMA has read them), columns
+        // rotated by the row in 16-byte pieces: 32 rows of a column piece then fall on different banks
+        if (wait_warp(bar(TFULL), 0, wc)) {
+            tc_fence_after();
+            const int row = (warp & 3) * 32 + lane;
+            const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                tmem_ld32(src + c * 32, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    st_shared_v4(base + row * 512 + (((c * 8 + q + row) & 31) << 4), v[4 * q], v[4 * q + 1], v[4 * q + 2],
+                                 v[4 * q + 3]);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR || splits > 1) cluster_sync_all();              // PAIR: no CTA leaves while its peer may signal it
+    tc_fence_after();
+    if (!PAIR && splits > 1) {
+        // rows rank, rank + splits, ... of the tile: one warp a row, four columns a lane, ranks in order
+        int r0, c0;
+        tile_of(first, r0, c0);
+        const int rows = min(128, p.rows - r0), col = c0 + lane * 4;
+        if (!*abort_flag && col < p.cols)
+            for (int r = rank + warp * splits; r < rows; r += (NTHREADS / 32) * splits) {
+                const uint32_t at = base + r * 512 + (((lane + r) & 31) << 4);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int z = 0; z < splits; ++z) {
+                    const uint4 v = ld_shared_cluster_v4(mapa_shared(at, z));
+                    acc = make_float4(acc.x + __uint_as_float(v.x), acc.y + __uint_as_float(v.y),
+                                      acc.z + __uint_as_float(v.z), acc.w + __uint_as_float(v.w));
+                }
+                *reinterpret_cast<uint2*>(p.out + static_cast<long long>(r0 + r) * p.cols + col) =
+                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+            }
+        __syncthreads();
+        cluster_sync_all();                                  // no CTA leaves while a peer reads its partial tile
+    }
+    if (warp == 1) {
+        if (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+        else
+            tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+template <bool A_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
+grad_pair_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_c, const Params p) {
+    grad_body<A_MN, true>(tma_a, tma_c, p);
+}
+template <bool A_MN>
+__global__ void __launch_bounds__(NTHREADS, 1)
+grad_split_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_c, const Params p) {
+    grad_body<A_MN, false>(tma_a, tma_c, p);
+}
+
+template <bool A_MN>
+int launch(const CUtensorMap& ta, const CUtensorMap& tc, const Params& p, cudaStream_t stream) {
+    auto tiles = [&](long long n) { return ((p.rows + n - 1) / n) * ((p.cols + n - 1) / n); };
+    const long long t256 = tiles(256), t128 = tiles(128);
+    // time in 256 x 256 tiles of a pair: a 128 x 128 tile takes a CTA half of one, at 70 % of the rate (it
+    // reads twice the shared memory per product)
+    if (static_cast<double>((t256 + 73) / 74) <= 0.5 / 0.7 * static_cast<double>((t128 + 147) / 148)) {
+        if (configure_smem(reinterpret_cast<const void*>(grad_pair_kernel<A_MN>), SMEM_BYTES) != 0) return -1;
+        grad_pair_kernel<A_MN><<<2 * static_cast<unsigned>(t256 < 74 ? t256 : 74), NTHREADS, SMEM_BYTES, stream>>>(ta, tc, p);
+        return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    }
+    if (configure_smem(reinterpret_cast<const void*>(grad_split_kernel<A_MN>), SMEM_BYTES) != 0) return -1;
+    // the terms are split while that still fits one CTA per SM and each has four stages or more
+    const int nk = (p.terms + BT - 1) / BT;
+    int splits = 1;
+    while (splits < 8 && 2 * splits * t128 <= 148 && nk / (2 * splits) >= 4) splits *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(splits, static_cast<unsigned>(t128 < 65535 ? t128 : 65535), static_cast<unsigned>((t128 + 65534) / 65535));
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, grad_split_kernel<A_MN>, ta, tc, p) == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace int8_grad
+
+int launch_int8_grad(const CUtensorMap& tdy, const CUtensorMap& tcodes, const float* scales, void* out, int rows, int cols,
+                     int terms, bool weight, unsigned long long budget_ns, int* status, cudaStream_t stream) {
+    const int8_grad::Params p{scales, static_cast<__nv_bfloat16*>(out), rows, cols, terms, budget_ns, status};
+    return weight ? int8_grad::launch<true>(tdy, tcodes, p, stream) : int8_grad::launch<false>(tdy, tcodes, p, stream);
 }
 
 }  // namespace wan
