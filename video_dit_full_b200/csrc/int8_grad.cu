@@ -4,13 +4,13 @@
 // a(t, r) = dY[r, t] for dX (t = output channels; the codes are the weight's).
 //
 // Bound by the bf16 tensor cores.  The codes stay 8 bits until they are in shared memory: TMA brings
-// [64 t][128 c] bytes, four converter warps multiply by the row's scale in fp32 and write bf16 into the
+// [64 t][128 c] bytes, converter warps multiply by the row's scale in fp32 and write bf16 into the
 // swizzled layout that the MMA reads, so the dequantised matrix never exists in memory (a pass of its
 // own would write and read 4 bytes for every code).  The one rounding on the way, x to bf16 (2^-8
 // relative at most), is what the tensor core's operand type costs; dY is used as it is, sums are fp32.
 // Byte to float costs one PRMT and half an add: the code + 128 goes under the exponent of 2^23.
 //
-// Two launches of the same roles (warp 0 TMA, 1 MMA, 2-5 epilogue, 6-9 converters; a stage holds A, the
+// Two launches of the same roles (warp 0 TMA of A, 1 MMA, 2-5 epilogue, 6-13 converters, 14 TMA of the codes; a stage holds A, the
 // codes and their bf16 form, 16 + 8 + 16 KB):
 //   PAIR   persistent CTA pairs (cta_group::2) on 256 x 256 tiles: each CTA converts its 128 columns of
 //          the pair's 256, half of what a CTA alone would have to for the same number of products
@@ -36,8 +36,11 @@ constexpr int OFF_TMEM_SLOT = OFF_BAR + NBARS * 8;
 constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
 constexpr int OFF_EPI = (OFF_ABORT + 8 + 15) & ~15;          // per epilogue warp: 32 rows x 64 B
 constexpr int EPI_WARP_BYTES = 32 * 64;
-constexpr int SMEM_BYTES = OFF_EPI + 4 * EPI_WARP_BYTES + 1024;
-constexpr int NTHREADS = 320;
+constexpr int GROUPS = 2;                                    // of four converter warps
+constexpr int WARP_CODES = 6 + 4 * GROUPS, NTHREADS = (WARP_CODES + 1) * 32;
+constexpr int SCALE_AHEAD = 4, SCALE_WARP_BYTES = SCALE_AHEAD * 64;         // per converter warp: 16 scales a stage
+constexpr int OFF_SCALES = OFF_EPI + 4 * EPI_WARP_BYTES;
+constexpr int SMEM_BYTES = OFF_SCALES + 4 * GROUPS * SCALE_WARP_BYTES + 1024;
 constexpr int GROUP = 16;                                    // tile order: row blocks in groups
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 static_assert(128 * 128 * 4 <= STAGES * STAGE_BYTES, "a partial tile reuses the stages");
@@ -74,6 +77,14 @@ __device__ __forceinline__ bool wait_thread_cluster(uint32_t bar, uint32_t parit
         if (done) return true;
         if (t0 == 0) t0 = global_timer_ns();
         if ((it & 15u) == 0 && wait_expired(w, t0)) return false;
+    }
+}
+
+// After an abort: the last `issued` copies counted on a ring's barriers land before the memory goes away.
+__device__ __forceinline__ void drain_ring(uint32_t bar0, Ring<STAGES> at, uint32_t issued) {
+    for (uint32_t i = 1; i <= issued; ++i) {
+        const int s = at.s >= static_cast<int>(i) ? at.s - i : at.s + STAGES - i;
+        drain_wait(bar0 + 8u * s, at.s >= static_cast<int>(i) ? at.use : at.use ^ 1u);
     }
 }
 
@@ -160,30 +171,24 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
 
     if (warp == 0) {
-        // ------------------------------ TMA producer ------------------------------
+        // ------------------------------ TMA producer of A -------------------------
         if (lane == 0) {
             tma_prefetch_desc(&tma_a);
-            tma_prefetch_desc(&tma_c);
-            int par[STAGES];
-            for (int s = 0; s < STAGES; ++s) par[s] = -1;
-            long long it = 0;
+            const uint32_t full0 = PAIR ? mapa_shared(bar(FULL), 0) : bar(FULL);
+            Ring<STAGES> ring;
+            uint32_t issued = 0;                             // stages whose copies may be in flight
             bool ok = true;
             for (long long t = first; t < tiles && ok; t += step) {
                 int r0, c0;
                 tile_of(t, r0, c0);
-                for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const int s = static_cast<int>(it % STAGES);
-                    const int use = static_cast<int>((it / STAGES) & 1);
-                    ok = wait_thread(bar(EMPTY + s), use ^ 1, wc);
+                int t0 = k0 * BT;
+                for (int kb = 0; kb < nk; ++kb, ring.next(), t0 += BT) {
+                    ok = wait_thread(bar(EMPTY + ring.s), ring.use ^ 1u, wc);
                     if (!ok) break;
-                    const uint32_t st = base + s * STAGE_BYTES;
-                    const int t0 = (k0 + kb) * BT;
-                    mbar_arrive_expect_tx(bar(CODES + s), C_BYTES);
-                    tma_load_2d(st + A_BYTES + B_BYTES, &tma_c, bar(CODES + s), c0, t0);
-                    if (leader) mbar_arrive_expect_tx(bar(FULL + s), CG * A_BYTES);
-                    // A: [64 t][2 x 64 r] (dW, MN-major) or [128 r][64 t] (dX, K-major)
+                    const uint32_t st = base + ring.s * STAGE_BYTES, full = full0 + 8u * ring.s;
+                    if (leader) mbar_arrive_expect_tx(bar(FULL + ring.s), CG * A_BYTES);
+                    // [64 t][2 x 64 r] (dW, MN-major) or [128 r][64 t] (dX, K-major)
                     if (PAIR) {
-                        const uint32_t full = mapa_shared(bar(FULL + s), 0);
                         if (A_MN) {
                             tma_load_2d_pair(st, &tma_a, full, r0, t0);
                             tma_load_2d_pair(st + HALF_BYTES, &tma_a, full, r0 + 64, t0);
@@ -191,26 +196,48 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
                             tma_load_2d_pair(st, &tma_a, full, t0, r0);
                         }
                     } else if (A_MN) {
-                        tma_load_2d(st, &tma_a, bar(FULL + s), r0, t0);
-                        tma_load_2d(st + HALF_BYTES, &tma_a, bar(FULL + s), r0 + 64, t0);
+                        tma_load_2d(st, &tma_a, full, r0, t0);
+                        tma_load_2d(st + HALF_BYTES, &tma_a, full, r0 + 64, t0);
                     } else {
-                        tma_load_2d(st, &tma_a, bar(FULL + s), t0, r0);
+                        tma_load_2d(st, &tma_a, full, t0, r0);
                     }
-                    par[s] = use;
+                    issued = min(issued + 1u, static_cast<uint32_t>(STAGES));
                 }
             }
-            if (!ok)
-                for (int s = 0; s < STAGES; ++s)
-                    if (par[s] >= 0) {
-                        drain_wait(bar(CODES + s), par[s]);
-                        if (leader) drain_wait(bar(FULL + s), par[s]);
-                    }
+            if (!ok && leader) drain_ring(bar(FULL), ring, issued);
+        }
+    } else if (warp == WARP_CODES) {
+        // ------------------------------ TMA producer of the codes -----------------
+        if (lane == 0) {
+            tma_prefetch_desc(&tma_c);
+            Ring<STAGES> ring;
+            uint32_t issued = 0;
+            bool ok = true;
+            for (long long t = first; t < tiles && ok; t += step) {
+                int r0, c0;
+                tile_of(t, r0, c0);
+                int t0 = k0 * BT;
+                for (int kb = 0; kb < nk; ++kb, ring.next(), t0 += BT) {
+                    ok = wait_thread(bar(EMPTY + ring.s), ring.use ^ 1u, wc);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(bar(CODES + ring.s), C_BYTES);
+                    tma_load_2d(base + ring.s * STAGE_BYTES + A_BYTES + B_BYTES, &tma_c, bar(CODES + ring.s), c0, t0);
+                    issued = min(issued + 1u, static_cast<uint32_t>(STAGES));
+                }
+            }
+            if (!ok) drain_ring(bar(CODES), ring, issued);
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer (a pair's leader) --------------
         if (lane == 0 && leader) {
             const uint32_t idesc = make_idesc(1, 1, 1, A_MN ? 1 : 0, 1, TILE, TILE);
-            long long it = 0;
+            // K-major: 16 terms are 32 bytes of a row; MN-major: 16 rows of 128 bytes, halves of the other
+            // axis HALF_BYTES apart.  The descriptors' high halves are the same, the low ones count 16 bytes.
+            constexpr uint32_t A_STEP = A_MN ? 128 : 2, B_STEP = 128;
+            const uint32_t hi = sdesc_hi();
+            const uint32_t a_lo = sdesc_lo(base, A_MN ? HALF_BYTES : 16), b_lo = sdesc_lo(base + A_BYTES, HALF_BYTES);
+            auto desc = [&](uint32_t lo) { return static_cast<uint64_t>(hi) << 32 | lo; };
+            Ring<STAGES> ring;
             int tc = 0;
             bool ok = true;
             for (long long t = first; t < tiles && ok; t += step, ++tc) {
@@ -219,38 +246,27 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + b * TILE;
-                for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const int s = static_cast<int>(it % STAGES);
-                    const uint32_t use = static_cast<uint32_t>((it / STAGES) & 1);
-                    ok = wait_thread(bar(FULL + s), use, wc);
-                    if (ok) ok = PAIR ? wait_thread_cluster(bar(READY + s), use, wc) : wait_thread(bar(READY + s), use, wc);
+                for (int kb = 0; kb < nk; ++kb, ring.next()) {
+                    const uint32_t st = ring.s * (STAGE_BYTES >> 4);
+                    ok = wait_thread(bar(FULL + ring.s), ring.use, wc);
+                    if (ok)
+                        ok = PAIR ? wait_thread_cluster(bar(READY + ring.s), ring.use, wc)
+                                  : wait_thread(bar(READY + ring.s), ring.use, wc);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sa = base + s * STAGE_BYTES, sb = sa + A_BYTES;
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk) {
-                        // K-major: 16 terms are 32 bytes of a row; MN-major: 16 rows of 128 bytes, halves
-                        // of the other axis HALF_BYTES apart
-                        const uint64_t a = A_MN ? sdesc_sw128(sa + kk * 2048, HALF_BYTES, 1024) : sdesc_sw128(sa + kk * 32, 16, 1024);
-                        const uint64_t bd = sdesc_sw128(sb + kk * 2048, HALF_BYTES, 1024);
+                        const uint64_t a = desc(a_lo + st + kk * A_STEP), bd = desc(b_lo + st + kk * B_STEP);
                         const uint32_t accumulate = (kb > 0 || kk > 0) ? 1u : 0u;
                         if (PAIR) mma_f16_ss_pair(acc, a, bd, idesc, accumulate);
                         else mma_f16_ss(acc, a, bd, idesc, accumulate);
                     }
-                    if (PAIR) {
-                        mma_commit_pair(bar(EMPTY + s));                     // both CTAs' stage s is free
-                        mma_commit_pair(mapa_shared(bar(EMPTY + s), 1));
-                    } else {
-                        mma_commit(bar(EMPTY + s));
-                    }
+                    if (PAIR) mma_commit_pair_both(bar(EMPTY + ring.s));     // both CTAs' stage is free
+                    else mma_commit(bar(EMPTY + ring.s));
                 }
                 if (!ok) break;
-                if (PAIR) {
-                    mma_commit_pair(bar(TFULL + b));
-                    mma_commit_pair(mapa_shared(bar(TFULL + b), 1));
-                } else {
-                    mma_commit(bar(TFULL + b));
-                }
+                if (PAIR) mma_commit_pair_both(bar(TFULL + b));
+                else mma_commit(bar(TFULL + b));
             }
             if (PAIR) mma_commit_pair(bar(DRAIN));
             else mma_commit(bar(DRAIN));
@@ -258,63 +274,70 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
         }
     } else if (warp >= 6) {
         // ------------------------------ converters --------------------------------
-        // Warp w of the four takes terms 16w .. 16w + 15 of a stage, four at a time: eight lanes read a
-        // term's 128 codes (16 each) and write them as two 16-byte chunks of its swizzled bf16 row.
-        const int w = warp - 6, sub = lane >> 3, ch = lane & 7;
+        // Groups of four warps take the stages in turn.  Warp w of a group takes terms 16w .. 16w + 15 of a
+        // stage, four at a time: eight lanes read a term's 128 codes (16 each) and write them as two 16-byte
+        // chunks of its swizzled bf16 row.  The terms' scales come SCALE_AHEAD stages early by cp.async.
+        const int cw = warp - 6, w = cw & 3, sub = lane >> 3, ch = lane & 7;
         const uint32_t odd = ch >> 2;                        // lanes 4-7 (the other half) write their chunks in
         const uint32_t ready = PAIR ? mapa_shared(bar(READY), 0) : bar(READY);   // reverse: no bank conflicts
-        float s_next[4];
-        auto load_scales = [&](int kb) {
+        const uint32_t ring = base + OFF_SCALES + cw * SCALE_WARP_BYTES;
+        const long long total = ((tiles - first + step - 1) / step) * nk;
+        auto fetch_scales = [&](long long it, int kb, int slot) {
+            if (it < total && lane < 16) {
+                const int t = (k0 + kb) * BT + w * 16 + lane;
+                const float* src = p.scales + min(t, p.terms - 1);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ring + slot * 64 + lane * 4), "l"(src),
+                             "r"(t < p.terms ? 4 : 0)        // zero behind the last term
+                             : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        auto after = [&](int kb) { return kb + GROUPS < nk ? kb + GROUPS : (kb + GROUPS) % nk; };
+        const int g = cw >> 2;
+        int kb_next = g % nk;                                // the stage whose scales are fetched next
+        for (int a = 0; a < SCALE_AHEAD; ++a, kb_next = after(kb_next)) fetch_scales(g + GROUPS * a, kb_next, a);
+        int slot = 0;
+        Ring<STAGES> stage;
+        for (int i = 0; i < g; ++i) stage.next();
+        for (long long it = g; it < total; it += GROUPS) {
+            const int s = stage.s;
+            asm volatile("cp.async.wait_group %0;" ::"n"(SCALE_AHEAD - 1) : "memory");
+            if (!wait_warp(bar(CODES + s), stage.use, wc)) break;
+            __syncwarp();                                    // every lane's copies are there for every lane
+            const uint32_t sb = base + s * STAGE_BYTES + A_BYTES;
+            const uint8_t* src = smem + s * STAGE_BYTES + A_BYTES + B_BYTES;
+            const float* sc = reinterpret_cast<const float*>(smem + OFF_SCALES + cw * SCALE_WARP_BYTES + slot * 64);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int t = (k0 + kb) * BT + w * 16 + q * 4 + sub;
-                s_next[q] = t < p.terms ? p.scales[t] : 0.f;
-            }
-        };
-        load_scales(0);
-        long long it = 0;
-        bool ok = true;
-        for (long long t = first; t < tiles && ok; t += step)
-            for (int kb = 0; kb < nk; ++kb, ++it) {
-                const int s = static_cast<int>(it % STAGES);
-                float sc[4];
+                const int row = w * 16 + q * 4 + sub;
+                const uint4 u = *reinterpret_cast<const uint4*>(src + row * 128 + ch * 16);
+                const uint32_t x[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
+                const float2 s2 = make_float2(sc[q * 4 + sub], sc[q * 4 + sub]);
+                uint32_t o[8];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) sc[q] = s_next[q];
-                load_scales(kb + 1 < nk ? kb + 1 : 0);       // the next stage's, behind this one's wait
-                ok = wait_warp(bar(CODES + s), static_cast<uint32_t>((it / STAGES) & 1), wc);
-                if (!ok) break;
-                const uint32_t sb = base + s * STAGE_BYTES + A_BYTES;
-                const uint8_t* src = smem + s * STAGE_BYTES + A_BYTES + B_BYTES;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int row = w * 16 + q * 4 + sub;
-                    const uint4 u = *reinterpret_cast<const uint4*>(src + row * 128 + ch * 16);
-                    const uint32_t x[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
-                    const float2 s2 = make_float2(sc[q], sc[q]);
-                    uint32_t o[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        o[2 * e] = scale2<0x7540, 0x7541>(x[e], s2);
-                        o[2 * e + 1] = scale2<0x7542, 0x7543>(x[e], s2);
-                    }
-                    const uint32_t half = sb + (ch >> 2) * HALF_BYTES;
-                    const int c0 = (ch & 3) * 2;
-                    const uint32_t a0 = sw128_chunk(half, row, c0), a1 = sw128_chunk(half, row, c0 + 1);
-                    if (odd) {
-                        st_shared_v4(a1, o[4], o[5], o[6], o[7]);
-                        st_shared_v4(a0, o[0], o[1], o[2], o[3]);
-                    } else {
-                        st_shared_v4(a0, o[0], o[1], o[2], o[3]);
-                        st_shared_v4(a1, o[4], o[5], o[6], o[7]);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    o[2 * e] = scale2<0x7540, 0x7541>(x[e], s2);
+                    o[2 * e + 1] = scale2<0x7542, 0x7543>(x[e], s2);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(ready + 8u * static_cast<uint32_t>(s));
-                    else mbar_arrive(ready + 8u * static_cast<uint32_t>(s));
-                }
+                const uint32_t half = sb + (ch >> 2) * HALF_BYTES;
+                const int c0 = (ch & 3) * 2;
+                const uint32_t a0 = sw128_chunk(half, row, c0 + odd), a1 = sw128_chunk(half, row, c0 + 1 - odd);
+                st_shared_v4(a0, odd ? o[4] : o[0], odd ? o[5] : o[1], odd ? o[6] : o[2], odd ? o[7] : o[3]);
+                st_shared_v4(a1, odd ? o[0] : o[4], odd ? o[1] : o[5], odd ? o[2] : o[6], odd ? o[3] : o[7]);
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster_relaxed_scope(ready + 8u * static_cast<uint32_t>(s));
+                else mbar_arrive(ready + 8u * static_cast<uint32_t>(s));
+            }
+            fetch_scales(it + GROUPS * SCALE_AHEAD, kb_next, slot);
+            kb_next = after(kb_next);
+            slot = slot + 1 < SCALE_AHEAD ? slot + 1 : 0;
+#pragma unroll
+            for (int i = 0; i < GROUPS; ++i) stage.next();
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (PAIR || splits == 1) {
         // ------------------------------ epilogue: this CTA's 128 rows -------------
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;

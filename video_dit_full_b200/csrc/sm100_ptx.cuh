@@ -534,6 +534,12 @@ __device__ __forceinline__ void cluster_sync_all() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
+// The same without the cluster-wide release, whose fence costs about a thousand cycles: for an arrival
+// that hands over nothing the other CTA's threads read (a tile that this CTA's own tensor core reads,
+// made visible to it by fence_proxy_async_smem before).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed_scope(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
 // TMA load into this CTA's shared memory whose completion is counted on a barrier of either
 // CTA of the pair (here always the leader's)
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, uint32_t bar_cluster, int c0,
@@ -551,6 +557,25 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar_cluster) {
                  : "memory");
 }
 
+// the same on the barriers at this shared::cta offset in both CTAs of the pair, with one instruction
+__device__ __forceinline__ void mma_commit_pair_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+// A position in a ring of N slots with one barrier each: the slot and the parity of its current use.
+template <int N>
+struct Ring {
+    int s = 0;
+    uint32_t use = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == N) {
+            s = 0;
+            use ^= 1u;
+        }
+    }
+};
 // 16 bytes of another CTA's shared memory (shared::cluster address).
 __device__ __forceinline__ uint4 ld_shared_cluster_v4(uint32_t addr) {
     uint4 v;
