@@ -345,13 +345,23 @@ def fp8_linear(x, w_codes, w_scale, stream=None):
     return fp8_gemm(codes, scales, w_codes, w_scale, stream=stream)
 
 
-def _check_device(**tensors):
-    """Every tensor on the current device (the one whose stream and context the call uses)."""
+def _call_stream(stream, device):
+    """The stream's handle as an integer; the current stream of `device` if none is given."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _same_device(first, **others):
+    """The index of the one device that every tensor is on, which must be the current one (the device
+    whose context and stream the call uses)."""
     import torch
     dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != dev:
+    if first.get_device() != dev:
+        raise ValueError(f"the tensors are on {first.device}, the current device is cuda:{dev}")
+    for name, t in others.items():
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return dev
 
 
 def _check_packed(name, t, shape=None):
@@ -363,38 +373,50 @@ def _check_packed(name, t, shape=None):
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, D]")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     T, H, D = t.shape
     row = H * D
-    ld = t.stride(0) if T > 1 else max(row, t.stride(0) // 8 * 8)
-    if t.numel() and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D) or ld < row or ld % 8):
+    if t.is_contiguous():
+        return row
+    ld, sh, sd = t.stride()
+    if T == 1:
+        ld = row                                   # one token: its stride means nothing
+    if (D > 1 and sd != 1) or (H > 1 and sh != D) or ld < row or ld % 8:
         raise ValueError(f"{name} must hold each token's [H, D] contiguously, tokens a multiple of 8 elements apart")
-    return ld if t.numel() else row
+    return ld
+
+
+def _check_offsets(name, t):
+    import torch
+    _check_plain(name, t, torch.int32)
+    if t.dim() != 1 or t.shape[0] < 2:
+        raise ValueError(f"{name} must be [sequences + 1]")
 
 
 def _check_packed_call(q, k, v, cu_q, cu_k):
-    import torch
     ldq, ldk = _check_packed("q", q), _check_packed("k", k)
     ldv = _check_packed("v", v, k.shape)
     Tq, H, D = q.shape
     Tk, Hkv, Dk = k.shape
     if Dk != D or Hkv < 1 or H % Hkv:
         raise ValueError(f"k has shape {tuple(k.shape)}: its heads must divide q's {H}, its D be {D}")
-    for name, t in (("cu_q", cu_q), ("cu_k", cu_k)):
-        _check_plain(name, t, torch.int32)
-        if t.dim() != 1 or t.numel() < 2:
-            raise ValueError(f"{name} must be [sequences + 1]")
-    if cu_q.numel() != cu_k.numel():
-        raise ValueError("cu_q and cu_k must name the same number of sequences")
-    return cu_q.numel() - 1, Tq, Tk, H, Hkv, D, ldq, ldk, ldv
+    _check_offsets("cu_q", cu_q)
+    if cu_k is not cu_q:
+        _check_offsets("cu_k", cu_k)
+        if cu_q.shape != cu_k.shape:
+            raise ValueError("cu_q and cu_k must name the same number of sequences")
+    return cu_q.shape[0] - 1, Tq, Tk, H, Hkv, D, ldq, ldk, ldv
 
 
-def _workspace(need, given, device):
+def _workspace(need, given, like):
+    """(pointer, bytes, tensor to keep) of the given workspace, or of a new one if the call needs any."""
     import torch
-    if given is None and need:
-        given = torch.empty(need, dtype=torch.uint8, device=device)
-    return (None, 0, None) if given is None else (given.data_ptr(), given.numel() * given.element_size(), given)
+    if given is None:
+        if not need:
+            return None, 0, None
+        given = like.new_empty(need, dtype=torch.uint8)
+    return given.data_ptr(), given.numel() * given.element_size(), given
 
 
 def varlen_fwd_workspace_size(N, Tq, Tk, H, Hkv, D=128) -> int:
@@ -408,16 +430,21 @@ def varlen_fwd(q, k, v, cu_q, cu_k, causal=False, o=None, lse=None, workspace=No
     Rows of a given o / lse outside every sequence keep what they held; without one they are undefined."""
     import torch
     N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv = _check_packed_call(q, k, v, cu_q, cu_k)
-    o = torch.empty((Tq, H, D), dtype=q.dtype, device=q.device) if o is None else o
-    _check_plain("o", o, torch.bfloat16, Tq * H * D)
-    lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device) if lse is None else lse
-    _check_plain("lse", lse, torch.float32, H * Tq)
-    _check_device(q=q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, o=o, lse=lse, workspace=workspace)
-    ws, ws_bytes, _keep = _workspace(varlen_fwd_workspace_size(N, Tq, Tk, H, Hkv, D), workspace, q.device)
-    _check("wan_attn_varlen_fwd",
-           lib().wan_attn_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                     cu_q.data_ptr(), cu_k.data_ptr(), N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv,
-                                     1 if causal else 0, ws, ws_bytes, _stream_ptr(stream)))
+    if o is None:
+        o = q.new_empty((Tq, H, D))
+    else:
+        _check_plain("o", o, torch.bfloat16, Tq * H * D)
+    if lse is None:
+        lse = q.new_empty((H, Tq), dtype=torch.float32)
+    else:
+        _check_plain("lse", lse, torch.float32, H * Tq)
+    dev = _same_device(q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, o=o, lse=lse, workspace=workspace)
+    so = lib()
+    ws, ws_bytes, _keep = _workspace(so.wan_attn_varlen_fwd_workspace_size(N, Tq, Tk, H, Hkv, D), workspace, q)
+    status = so.wan_attn_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                    cu_q.data_ptr(), cu_k.data_ptr(), N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv,
+                                    1 if causal else 0, ws, ws_bytes, _call_stream(stream, dev))
+    _check("wan_attn_varlen_fwd", status)
     return o, lse
 
 
@@ -433,18 +460,20 @@ def varlen_bwd(q, k, v, o, do, lse, cu_q, cu_k, causal=False, dq=None, dk=None, 
     _check_plain("o", o, torch.bfloat16, Tq * H * D)
     _check_plain("do", do, torch.bfloat16, Tq * H * D)
     _check_plain("lse", lse, torch.float32, H * Tq)
-    dq = torch.empty((Tq, H, D), dtype=q.dtype, device=q.device) if dq is None else dq
-    dk = torch.empty((Tk, Hkv, D), dtype=q.dtype, device=q.device) if dk is None else dk
-    dv = torch.empty((Tk, Hkv, D), dtype=q.dtype, device=q.device) if dv is None else dv
+    dq = q.new_empty((Tq, H, D)) if dq is None else dq
+    dk = q.new_empty((Tk, Hkv, D)) if dk is None else dk
+    dv = q.new_empty((Tk, Hkv, D)) if dv is None else dv
     lddq = _check_packed("dq", dq, q.shape)
     lddk, lddv = _check_packed("dk", dk, k.shape), _check_packed("dv", dv, k.shape)
-    _check_device(q=q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, o=o, do=do, lse=lse, dq=dq, dk=dk, dv=dv, workspace=workspace)
-    ws, ws_bytes, _keep = _workspace(varlen_bwd_workspace_size(N, Tq, Tk, H, Hkv, D), workspace, q.device)
-    _check("wan_attn_varlen_bwd",
-           lib().wan_attn_varlen_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
-                                     lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_q.data_ptr(),
-                                     cu_k.data_ptr(), N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv, lddq, lddk, lddv,
-                                     1 if causal else 0, ws, ws_bytes, _stream_ptr(stream)))
+    dev = _same_device(q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, o=o, do=do, lse=lse, dq=dq, dk=dk, dv=dv,
+                       workspace=workspace)
+    so = lib()
+    ws, ws_bytes, _keep = _workspace(so.wan_attn_varlen_bwd_workspace_size(N, Tq, Tk, H, Hkv, D), workspace, q)
+    status = so.wan_attn_varlen_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_q.data_ptr(),
+                                    cu_k.data_ptr(), N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv, lddq, lddk, lddv,
+                                    1 if causal else 0, ws, ws_bytes, _call_stream(stream, dev))
+    _check("wan_attn_varlen_bwd", status)
     return dq, dk, dv
 
 
@@ -455,7 +484,7 @@ def _check_matrix(name, t, dtype, cols=None):
         raise ValueError(f"{name} must be 2-D")
     if cols is not None and t.shape[1] != cols:
         raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
-    return tuple(t.shape)
+    return t.shape
 
 
 def _check_activations(x):
@@ -466,10 +495,14 @@ def _check_activations(x):
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
-    ld = x.stride(0) if M > 1 else max(K, x.stride(0) // 8 * 8)
-    if x.numel() and ((K > 1 and x.stride(1) != 1) or ld < K or ld % 8):
+    if x.is_contiguous():
+        return M, K, K
+    ld, sk = x.stride()
+    if M == 1:
+        ld = K                                     # one row: its stride means nothing
+    if (K > 1 and sk != 1) or ld < K or ld % 8:
         raise ValueError("x must hold each row contiguously, rows a multiple of 8 elements apart")
-    return M, K, ld if x.numel() else K
+    return M, K, ld
 
 
 def int8_quantize_rows(x, codes=None, scales=None, stream=None):
@@ -477,13 +510,13 @@ def int8_quantize_rows(x, codes=None, scales=None, stream=None):
     an activation's 8-bit checkpoint, or a weight [N, K] with a scale per output channel."""
     import torch
     M, K, ldx = _check_activations(x)
-    codes = torch.empty((M, K), dtype=torch.int8, device=x.device) if codes is None else codes
-    scales = torch.empty(M, dtype=torch.float32, device=x.device) if scales is None else scales
+    codes = x.new_empty((M, K), dtype=torch.int8) if codes is None else codes
+    scales = x.new_empty(M, dtype=torch.float32) if scales is None else scales
     _check_plain("codes", codes, torch.int8, M * K)
     _check_plain("scales", scales, torch.float32, M)
-    _check_device(x=x, codes=codes, scales=scales)
+    dev = _same_device(x, codes=codes, scales=scales)
     _check("wan_int8_quantize_rows", lib().wan_int8_quantize_rows(x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-                                                                  M, K, ldx, _stream_ptr(stream)))
+                                                                  M, K, ldx, _call_stream(stream, dev)))
     return codes, scales
 
 
@@ -492,11 +525,11 @@ def int8_dequantize_rows(codes, scales, x=None, stream=None):
     import torch
     M, K = _check_matrix("codes", codes, torch.int8)
     _check_plain("scales", scales, torch.float32, M)
-    x = torch.empty((M, K), dtype=torch.bfloat16, device=codes.device) if x is None else x
+    x = codes.new_empty((M, K), dtype=torch.bfloat16) if x is None else x
     _check_plain("x", x, torch.bfloat16, M * K)
-    _check_device(codes=codes, scales=scales, x=x)
+    dev = _same_device(codes, scales=scales, x=x)
     _check("wan_int8_dequantize_rows", lib().wan_int8_dequantize_rows(codes.data_ptr(), scales.data_ptr(),
-                                                                      x.data_ptr(), M, K, _stream_ptr(stream)))
+                                                                      x.data_ptr(), M, K, _call_stream(stream, dev)))
     return x
 
 
@@ -515,12 +548,12 @@ def int8_gemm(a_codes, a_scales, w_codes, w_scales, bias=None, y=None, stream=No
     M, K = _check_matrix("a_codes", a_codes, torch.int8)
     _check_plain("a_scales", a_scales, torch.float32, M)
     N = _check_weight(w_codes, w_scales, bias, K)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=a_codes.device) if y is None else y
+    y = a_codes.new_empty((M, N), dtype=torch.bfloat16) if y is None else y
     _check_plain("y", y, torch.bfloat16, M * N)
-    _check_device(a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales, bias=bias, y=y)
+    dev = _same_device(a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales, bias=bias, y=y)
     _check("wan_int8_gemm", lib().wan_int8_gemm(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(),
                                                 w_scales.data_ptr(), None if bias is None else bias.data_ptr(),
-                                                y.data_ptr(), M, N, K, _stream_ptr(stream)))
+                                                y.data_ptr(), M, N, K, _call_stream(stream, dev)))
     return y
 
 
@@ -531,14 +564,14 @@ def int8_linear(x, w_codes, w_scales, bias=None, return_checkpoint=False, stream
     import torch
     M, K, ldx = _check_activations(x)
     N = _check_weight(w_codes, w_scales, bias, K)
-    codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    scales = torch.empty(M, dtype=torch.float32, device=x.device)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    _check_device(x=x, w_codes=w_codes, w_scales=w_scales, bias=bias)
+    y = x.new_empty((M, N))
+    codes = x.new_empty((M, K), dtype=torch.int8)
+    scales = x.new_empty(M, dtype=torch.float32)
+    dev = _same_device(x, w_codes=w_codes, w_scales=w_scales, bias=bias)
     _check("wan_int8_linear", lib().wan_int8_linear(x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
                                                     None if bias is None else bias.data_ptr(), y.data_ptr(),
                                                     codes.data_ptr(), scales.data_ptr(), M, N, K, ldx,
-                                                    _stream_ptr(stream)))
+                                                    _call_stream(stream, dev)))
     return (y, codes, scales) if return_checkpoint else y
 
 
@@ -547,15 +580,15 @@ def int8_grad_weight(dy, codes, scales, dw=None, stream=None):
     (``wan_int8_grad_weight``)."""
     import torch
     M, N = _check_matrix("dy", dy, torch.bfloat16)
-    _, K = _check_matrix("codes", codes, torch.int8)
-    if codes.shape[0] != M:
-        raise ValueError(f"codes has {codes.shape[0]} rows, dy {M}")
+    rows, K = _check_matrix("codes", codes, torch.int8)
+    if rows != M:
+        raise ValueError(f"codes has {rows} rows, dy {M}")
     _check_plain("scales", scales, torch.float32, M)
-    dw = torch.empty((N, K), dtype=torch.bfloat16, device=dy.device) if dw is None else dw
+    dw = dy.new_empty((N, K)) if dw is None else dw
     _check_plain("dw", dw, torch.bfloat16, N * K)
-    _check_device(dy=dy, codes=codes, scales=scales, dw=dw)
+    dev = _same_device(dy, codes=codes, scales=scales, dw=dw)
     _check("wan_int8_grad_weight", lib().wan_int8_grad_weight(dy.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-                                                              dw.data_ptr(), M, N, K, _stream_ptr(stream)))
+                                                              dw.data_ptr(), M, N, K, _call_stream(stream, dev)))
     return dw
 
 
@@ -568,11 +601,11 @@ def int8_grad_input(dy, w_codes, w_scales, dx=None, stream=None):
     if rows != N:
         raise ValueError(f"w_codes has {rows} rows, dy {N} columns")
     _check_plain("w_scales", w_scales, torch.float32, N)
-    dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device) if dx is None else dx
+    dx = dy.new_empty((M, K)) if dx is None else dx
     _check_plain("dx", dx, torch.bfloat16, M * K)
-    _check_device(dy=dy, w_codes=w_codes, w_scales=w_scales, dx=dx)
+    dev = _same_device(dy, w_codes=w_codes, w_scales=w_scales, dx=dx)
     _check("wan_int8_grad_input", lib().wan_int8_grad_input(dy.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
-                                                            dx.data_ptr(), M, N, K, _stream_ptr(stream)))
+                                                            dx.data_ptr(), M, N, K, _call_stream(stream, dev)))
     return dx
 
 
