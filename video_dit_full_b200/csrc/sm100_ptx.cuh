@@ -564,6 +564,28 @@ __device__ __forceinline__ void mma_commit_pair_both(uint32_t bar) {
         "h"(static_cast<uint16_t>(3))
         : "memory");
 }
+// Cluster launch control: ask for a block of this grid that has not started yet (16 bytes of answer to
+// shared memory at `dst`, counted on `bar`).  No request may follow one that was refused.
+__device__ __forceinline__ void clc_try_cancel(uint32_t dst, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+                 "r"(bar)
+                 : "memory");
+}
+// The answer: true and the block's index, which this block now stands in for, or false.
+__device__ __forceinline__ bool clc_answer(uint32_t src, int& x, int& y) {
+    uint32_t got, bx = 0, by = 0;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%3];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, _, _}, r;\n\t}"
+        : "=&r"(got), "=&r"(bx), "=&r"(by)
+        : "r"(src)
+        : "memory");
+    x = static_cast<int>(bx);
+    y = static_cast<int>(by);
+    return got != 0;
+}
 // A position in a ring of N slots with one barrier each: the slot and the parity of its current use.
 template <int N>
 struct Ring {
