@@ -26,6 +26,9 @@
 //   - the last key block may hold the next sequence's rows: its K only meets masked scores, its V rows
 //     are zeroed in shared memory before the tensor core reads them (0 x NaN is NaN)
 //   - a tile that the sequence does not fill is stored row by row; the rows behind it are not touched
+//   - an item with a single Q tile (a generated token, a sequence's last rows) has both groups work on it,
+//     each on every other key block with a running m, l and O of its own, joined at the end in TMEM: one
+//     group alone would leave the memory idle between its scores and its products
 //   - few query rows against many keys: gridDim.y items split the keys and a second kernel joins their
 //     normalised fp32 partial results by their lse
 #include <cuda.h>
@@ -49,9 +52,10 @@ constexpr int OFF_WORK = OFF_V + 2 * TILE_BYTES;   // two work slots
 constexpr int WORK_BYTES = 64;
 constexpr int AHEAD = 6;                           // key blocks left of an item when the next one is fetched
 constexpr int OFF_CLC = OFF_WORK + 2 * WORK_BYTES; // cluster launch control's answer
-constexpr int OFF_BAR = OFF_CLC + 16;
+constexpr int OFF_ML = OFF_CLC + 16;               // m and l of tile 1's rows, for the join of a shared tile
+constexpr int OFF_BAR = OFF_ML + 2 * BM * 4;
 enum Bar { Q_FULL = 0, Q_EMPTY = 2, K_FULL = 4, K_EMPTY = 6, V_FULL = 8, V_EMPTY = 10, S_FULL = 12, P_FULL = 14,
-           O_FINAL = 16, W_FULL = 18, W_EMPTY = 20, V_TAIL = 22, CLC = 23, NEXT = 24, DRAIN = 25, NBARS = 26 };
+           O_FINAL = 16, W_FULL = 18, W_EMPTY = 20, V_TAIL = 22, CLC = 23, NEXT = 24, ML_READY = 25, ML_DONE = 26, DRAIN = 27, NBARS = 28 };
 constexpr int OFF_TMEM_SLOT = OFF_BAR + NBARS * 8;
 constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
 constexpr int SMEM_BYTES = OFF_ABORT + 8 + 1024;   // slack for 1024-byte alignment of the tiles
@@ -64,6 +68,7 @@ constexpr float RESCALE_THRESHOLD = 8.0f;      // log2 units: keep a stale max w
 struct Work {
     int n;                 // key blocks of this item; -1: there is no more work
     int nt[2];             // key blocks of each tile, 0 for a tile without rows or keys here
+    int shared;            // both tiles are the same rows: tile t takes the item's blocks t, t + 2, ...
     int j0;                // first key block
     int h0;                // first query head of the packed group
     int q_begin, q_len;    // the sequence's rows on the query axis
@@ -121,6 +126,8 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         mbar_init(bar(V_TAIL), 1);
         mbar_init(bar(CLC), 1);
         mbar_init(bar(NEXT), 1);
+        mbar_init(bar(ML_READY), 4);
+        mbar_init(bar(ML_DONE), 4);
         mbar_init(bar(DRAIN), 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -165,9 +172,11 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                 if (!wait_warp(bar(W_EMPTY + (item & 1u)), ((item >> 1) & 1u) ^ 1u, wc)) break;
                 if (lane == 0) {
                     volatile Work* w = slot_of(item);
+                    const bool shared = i0 + tile_tokens >= sq.len && n > 1;
                     w->n = n;
-                    w->nt[0] = min(max(nblk[0] - j0, 0), n);
-                    w->nt[1] = min(max(nblk[1] - j0, 0), n);
+                    w->nt[0] = shared ? (n + 1) / 2 : min(max(nblk[0] - j0, 0), n);
+                    w->nt[1] = shared ? n / 2 : min(max(nblk[1] - j0, 0), n);
+                    w->shared = shared ? 1 : 0;
                     w->j0 = j0;
                     w->h0 = x % packed_heads * p.pack;
                     w->q_begin = sq.begin;
@@ -221,7 +230,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
             if (n < 0) break;
             const int j0 = w->j0, k_begin = w->k_begin, h0 = w->h0, hk = h0 / (p.H / p.Hkv);
             const int q_tok = w->q_begin + w->i0;
-            const int nt[2] = {w->nt[0], w->nt[1]};
+            const int nt[2] = {w->nt[0], w->nt[1]}, tok1 = w->shared ? 0 : tile_tokens;      // tile 1's first token
             // rows of the last block that lie behind the sequence (only a sequence's last block has any)
             const int tail = n > 0 ? max((j0 + n) * BN - w->k_len, 0) : 0;
             const int whole = n - (tail > 0 ? 1 : 0);
@@ -245,8 +254,8 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                         ok = wait_thread(bar(Q_EMPTY + t), (loads[t] & 1u) ^ 1u, wc);
                         if (!ok) break;
                         mbar_arrive_expect_tx(bar(Q_FULL + t), qbytes);
-                        tma_load_3d(sQ + t * TILE_BYTES, &tmq, bar(Q_FULL + t), 0, h0, q_tok + t * tile_tokens);
-                        tma_load_3d(sQ + t * TILE_BYTES + HALF_BYTES, &tmq, bar(Q_FULL + t), 64, h0, q_tok + t * tile_tokens);
+                        tma_load_3d(sQ + t * TILE_BYTES, &tmq, bar(Q_FULL + t), 0, h0, q_tok + t * tok1);
+                        tma_load_3d(sQ + t * TILE_BYTES + HALF_BYTES, &tmq, bar(Q_FULL + t), 64, h0, q_tok + t * tok1);
                         ++loads[t];
                     }
                     if (!ok) break;
@@ -308,10 +317,39 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                 ok = wait_thread(bar(W_FULL + (item & 1u)), (item >> 1) & 1u, wc);
                 if (!ok) break;
                 volatile Work* w = slot_of(item);
-                const int n = w->n, nt[2] = {w->nt[0], w->nt[1]};
+                const int n = w->n, nt[2] = {w->nt[0], w->nt[1]}, shared = w->shared;
                 if (n < 0) break;
                 mbar_arrive(bar(W_EMPTY + (item & 1u)));
                 if (n == 0) continue;
+                if (shared) {
+                    // block i is tile i & 1's alone; a tile's next scores follow its products
+                    auto scores = [&](int t, uint32_t at) {
+                        if (!wait_thread(bar(K_FULL + (at & 1u)), (at >> 1) & 1u, wc)) return false;
+                        tc_fence_after();
+                        issue_qk(t, at & 1u);
+                        mma_commit(bar(S_FULL + t));
+                        mma_commit(bar(K_EMPTY + (at & 1u)));
+                        return true;
+                    };
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        ok = wait_thread(bar(Q_FULL + t), (loads >> t) & 1u, wc);
+                        loads ^= 1u << t;
+                        if (ok) ok = scores(t, kv + t);
+                    }
+                    for (int i = 0; i < n && ok; ++i, ++kv) {
+                        const int t = i & 1;
+                        ok = wait_thread(bar(V_FULL + (kv & 1u)), (kv >> 1) & 1u, wc);
+                        if (ok) ok = wait_thread(bar(P_FULL + t), (blocks >> t) & 1u, wc);
+                        if (!ok) break;
+                        blocks ^= 1u << t;
+                        tc_fence_after();
+                        issue_pv(t, kv & 1u, i > 1);
+                        mma_commit(bar(V_EMPTY + (kv & 1u)));
+                        if (i + 2 < n) ok = scores(t, kv + 2);
+                        else mma_commit(bar(O_FINAL + t));
+                    }
+                    continue;
+                }
                 ok = wait_thread(bar(K_FULL + (kv & 1u)), (kv >> 1) & 1u, wc);
                 if (!ok) break;
 #pragma unroll
@@ -369,23 +407,25 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         const uint32_t tS = tmem + t * BN + lane_off;
         const uint32_t tO = tmem + 256 + t * HD + lane_off;
         const float c = p.scale_log2;
-        uint32_t st = 0;                         // bit 0: parity of S_FULL, bit 1: of O_FINAL, above: the item's number
-        for (;; st += 4u) {
+        uint32_t st = 0;                         // parity bits: 1 S_FULL, 2 O_FINAL, 4 ML_*; above: the item's number
+        for (;; st += 8u) {
             // the item's slot is kept until its epilogue is done: only what the loop needs is in registers
-            bool ok = wait_warp(bar(W_FULL + ((st >> 2) & 1u)), (st >> 3) & 1u, wc);
-            uint32_t w = base + OFF_WORK + ((st >> 2) & 1u) * WORK_BYTES;
-            if (!ok || WORK(w, n) < 0) break;
+            bool ok = wait_warp(bar(W_FULL + ((st >> 3) & 1u)), (st >> 4) & 1u, wc);
+            named_bar_sync(1 + t, BM);           // the group's warps go on together or not at all:
+            if (*abort_flag) break;              // one that gave up set the flag before the barrier
+            uint32_t w = base + OFF_WORK + ((st >> 3) & 1u) * WORK_BYTES;
+            if (WORK(w, n) < 0) break;
             const int nt = t ? WORK(w, nt[1]) : WORK(w, nt[0]);
             int keys;                            // keys that the row sees, counted from the item's first block
             {
                 const int row_tok = fresh(threadIdx.x & 127) / p.pack;
-                const int i_tok = WORK(w, i0) + t * tile_tokens + row_tok, k_len = WORK(w, k_len), q_len = WORK(w, q_len);
+                const int i_tok = WORK(w, i0) + (WORK(w, shared) ? 0 : t * tile_tokens) + row_tok, k_len = WORK(w, k_len), q_len = WORK(w, q_len);
                 const bool real = row_tok < tile_tokens && i_tok < q_len;
                 keys = !real ? 0 : p.causal ? min(max(i_tok + k_len - q_len + 1, 0), k_len) : k_len;
-                keys -= WORK(w, j0) * BN;
+                keys -= (WORK(w, j0) + (WORK(w, shared) ? t : 0)) * BN;       // ... from the tile's first block
             }
             float m_ref = -INFINITY, l = 0.f;
-            for (int i = 0; i < nt; ++i) {
+            for (int i = 0; i < nt; ++i, keys -= WORK(w, shared) ? 2 * BN : BN) {
                 ok = wait_warp(bar(S_FULL + t), st & 1u, wc);
                 if (!ok) break;
                 st ^= 1u;
@@ -395,11 +435,10 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                 for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[q * 32]));
                 tmem_wait_ld();
                 float* s = reinterpret_cast<float*>(sr);
-                const int valid = keys - i * BN;     // keys of this block that the row sees
-                if (__any_sync(0xffffffffu, valid < BN)) {
+                if (__any_sync(0xffffffffu, keys < BN)) {     // the row sees the first `keys` of this block
 #pragma unroll
                     for (int q = 0; q < 128; ++q)
-                        if (q >= valid) s[q] = -INFINITY;
+                        if (q >= keys) s[q] = -INFINITY;
                 }
                 // row max: 8 chains of three-input maxima, then a short tree
                 float m8[8];
@@ -461,17 +500,42 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
             }
             // A whole tile leaves through its Q buffer (every MMA that read it has completed) and two TMA
             // stores; a tile that the sequence does not fill, or a split's partial result, row by row.
-            w = base + OFF_WORK + ((static_cast<uint32_t>(fresh(st)) >> 2) & 1u) * WORK_BYTES;
+            w = base + OFF_WORK + ((static_cast<uint32_t>(fresh(st)) >> 3) & 1u) * WORK_BYTES;
             const int r = fresh(threadIdx.x & 127);       // row within the tile = TMEM lane
-            const int row_tok = r / p.pack, i_tile = WORK(w, i0) + t * tile_tokens, q_len = WORK(w, q_len);
+            const bool shared = WORK(w, shared) != 0;
+            float a0 = 1.f, a1 = 0.f;                     // what the two tiles' O count when a shared tile is joined
+            if (shared) {
+                float* ml = reinterpret_cast<float*>(smem + OFF_ML) + r;
+                if (t == 1) {
+                    ml[0] = m_ref;
+                    ml[BM] = l;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(ML_READY));
+                    if (ok) ok = wait_warp(bar(ML_DONE), (st >> 2) & 1u, wc);
+                } else {
+                    if (ok) ok = wait_warp(bar(ML_READY), (st >> 2) & 1u, wc);
+                    if (ok) {
+                        const float m1 = ml[0], m = fmaxf(m_ref, m1);
+                        a0 = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
+                        a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
+                        l = l * a0 + ml[BM] * a1;
+                        m_ref = m;
+                    }
+                }
+                st ^= 4u;
+            }
+            const int row_tok = r / p.pack, i_tile = WORK(w, i0) + (shared ? 0 : t * tile_tokens), q_len = WORK(w, q_len);
             const int head = WORK(w, h0) + r - row_tok * p.pack, token = WORK(w, q_begin) + i_tile + row_tok;
-            const bool real = row_tok < tile_tokens && i_tile + row_tok < q_len;
+            const bool real = row_tok < tile_tokens && i_tile + row_tok < q_len && !(shared && t == 1);
             const bool empty = m_ref == -INFINITY;            // the row saw no key here
-            const bool by_tma = p.splits == 1 && i_tile + tile_tokens <= q_len && nt > 0;
+            const bool by_tma = p.splits == 1 && i_tile + tile_tokens <= q_len && nt > 0 && !shared;
             const uint32_t stage = sQ + t * TILE_BYTES;
-            if (ok) {
+            if (ok && !(shared && t == 1)) {
                 tc_fence_after();
                 const float inv_l = empty ? 0.f : 1.f / l;
+                a0 *= inv_l;
+                a1 *= inv_l;
                 const long long row = static_cast<long long>(token) * p.H + head;
                 const long long part = static_cast<long long>(WORK(w, split)) * p.Tq * p.H;
 #pragma unroll 1
@@ -482,7 +546,15 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                         tmem_wait_ld();
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = empty ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv_l);
+                    for (int e = 0; e < 32; ++e) o[e] = empty ? 0u : __float_as_uint(__uint_as_float(o[e]) * a0);
+                    if (shared) {
+                        uint32_t o1[32];
+                        tmem_ld32(tO + HD + q * 32, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (a1 != 0.f) o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), a1, __uint_as_float(o[e])));
+                    }
                     if (p.splits > 1) {
                         if (real && !empty) {
                             uint4* dst = reinterpret_cast<uint4*>(p.o_part + (part + row) * HD + q * 32);
@@ -509,6 +581,10 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                     }
                 }
                 tc_fence_before();                            // O is read: the next item's products may overwrite it
+                if (shared) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(ML_DONE));
+                }
                 fence_proxy_async_smem();
                 if (real) {
                     const float lse2 = empty ? -INFINITY : m_ref + log2f(l);
@@ -519,7 +595,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
             }
             const int q_begin = WORK(w, q_begin), h0 = WORK(w, h0);
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(W_EMPTY + ((st >> 2) & 1u)));
+            if (lane == 0) mbar_arrive(bar(W_EMPTY + ((st >> 3) & 1u)));
             named_bar_sync(1 + t, BM);                // every warp of the group, whatever its state
             if (*abort_flag) break;                   // a warp that gave up set it before the barrier
             if (r == 0 && nt > 0) {
@@ -580,8 +656,10 @@ static long long tile_bound(int N, int Tq, int pack) {
 }  // namespace varlen
 
 // pack: the most heads of a group that fill at least 120 of a tile's 128 rows (128 / pack tokens of
-// `pack` heads each).  splits: when the tiles alone do not fill the GPU, as many CTAs as give it two
-// waves, of 4 key blocks at least on average.
+// `pack` heads each).  splits: a tile's keys go to several items when there are fewer than two tiles for
+// every SM, enough to make two; and when the sequences are single tiles on average (generated tokens:
+// memory bound, lengths anything), enough to make eight, so that the longest sequence's items do not
+// outlast the rest.  An item keeps 4 key blocks on average.
 void varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv, int* pack, int* splits) {
     const int group = H / Hkv;
     int pk = 1;
@@ -590,7 +668,8 @@ void varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv, int* pack, int* spli
     *pack = pk;
     const long long ctas = varlen::tile_bound(N, Tq, pk) * (H / pk);
     const long long blocks = (static_cast<long long>(Tk) / N + varlen::BN - 1) / varlen::BN;
-    long long s = ctas > 0 && ctas < 2 * 148 ? (2 * 148 + ctas - 1) / ctas : 1;
+    const long long want = (static_cast<long long>(Tq) <= static_cast<long long>(N) * (varlen::BM / pk) ? 8 : 2) * 148;
+    long long s = ctas > 0 && ctas < want ? (want + ctas - 1) / ctas : 1;
     if (s > blocks / 4) s = blocks / 4;
     if (s > 64) s = 64;
     *splits = s < 1 ? 1 : static_cast<int>(s);
