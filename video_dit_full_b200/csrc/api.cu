@@ -822,7 +822,8 @@ int wan_attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, fl
 
 size_t wan_attn_varlen_bwd_workspace_size(int N, int Tq, int Tk, int H, int Hkv, int D) {
     if (check_packed(N, Tq, Tk, H, Hkv, D) != WAN_ATTN_OK) return 0;
-    size_t bytes = align256(size_t(Tq) * H * 128 * 4) + align256(size_t(Tq) * H * 4);
+    size_t bytes = align256(size_t(Tq) * H * 128 * 4) + align256(size_t(Tq) * H * 4) +
+                   align256(size_t(varlen_bwd_tile_bound(N, Tk)) * 8) + align256(size_t(N) * 4);
     if (varlen_bwd_splits(N, Tq, Tk, H, Hkv) > 1) bytes += 2 * align256(size_t(Tk) * Hkv * 128 * 4);
     return bytes;
 }
@@ -861,9 +862,13 @@ int wan_attn_varlen_bwd(const void* q, const void* k, const void* v, const void*
     p.lddv = lddv;
     p.splits = varlen_bwd_splits(N, Tq, Tk, H, Hkv);
     char* ws = static_cast<char*>(workspace);
-    const size_t off_delta = align256(size_t(Tq) * H * 128 * 4), off_dk = off_delta + align256(size_t(Tq) * H * 4);
+    p.tile_bound = varlen_bwd_tile_bound(N, Tk);
+    const size_t off_delta = align256(size_t(Tq) * H * 128 * 4), off_order = off_delta + align256(size_t(Tq) * H * 4);
+    const size_t off_end = off_order + align256(size_t(p.tile_bound) * 8), off_dk = off_end + align256(size_t(N) * 4);
     p.dq_acc = reinterpret_cast<float*>(ws);
     p.delta = reinterpret_cast<float*>(ws + off_delta);
+    p.order = reinterpret_cast<int2*>(ws + off_order);
+    p.tile_end = reinterpret_cast<int*>(ws + off_end);
     if (p.splits > 1) {
         p.dk_acc = reinterpret_cast<float*>(ws + off_dk);
         p.dv_acc = reinterpret_cast<float*>(ws + off_dk + align256(size_t(Tk) * Hkv * 128 * 4));

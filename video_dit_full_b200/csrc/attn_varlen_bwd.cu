@@ -6,7 +6,8 @@
 //     dV = P^T dO,  dK = dS^T Q / sqrt(D),  dQ = dS K / sqrt(D);  dK, dV summed over a group's query heads.
 //
 // Three kernels:
-//   varlen_prep  D_i (fp32) and zeroing of the fp32 dQ accumulator
+//   varlen_prep  D_i (fp32), zeroing of the fp32 dQ accumulator, and (one block) the key tiles of all
+//                sequences in the order of their work, most first
 //   varlen_main  one CTA per 128-key tile of a sequence and kv head.  K_j and V_j stay in shared memory
 //                while the CTA walks the 128-row Q tiles that see any of its keys, of every query head of
 //                the group in turn: dK and dV gather the group's sum in TMEM, with no atomics.  Per Q tile
@@ -15,8 +16,9 @@
 //                  S^T = K Q^T, dP^T = V dO^T;  dV += P^T dO;  dK += dS^T Q;  dQ^T = K^T dS^T -> TMA reduce-add
 //   varlen_cast  dQ (and split dK, dV) = bf16(accumulator x scale), rows of the sequences only
 // What packing adds:
-//   - causal: Q tiles before the diagonal are never loaded; a sequence's first key tiles, which meet the
-//     most queries, start first
+//   - causal: Q tiles before the diagonal are never loaded; key tiles then differ by the length of a
+//     sequence in Q tiles, so the ones with most start first, of every kv head in turn (head by head the
+//     last head's longest tile started late: 571 us against 443 for the packed documents of the benchmark)
 //   - pairs that do not see each other get P = 0 and dS = 0 by selection, never by arithmetic, so that an
 //     infinite or NaN score, lse or dP there leaves no trace (diagonal and edge tiles only)
 //   - rows behind the sequence in an edge tile belong to another one: K, Q and dO rows there are zeroed in
@@ -33,8 +35,6 @@ namespace varlen_bwd {
 
 using varlen::Span;
 using varlen::span_of;
-using varlen::TileAt;
-using varlen::tile_at;
 
 constexpr int BM = 128;                  // keys per CTA and queries per Q tile
 constexpr int HD = 128;
@@ -88,6 +88,14 @@ __device__ __forceinline__ void mma_ss_mn(uint32_t d, uint32_t a, uint32_t b, ui
     mma8_f16_ss<512, 128>(d, sdesc_lo(a, HALF_BYTES), sdesc_lo(b, HALF_BYTES), hi, idesc, 0u);
 }
 
+// The first Q tile that sees any key of key tile `tile` of a sequence, and how many do.
+__device__ __forceinline__ int first_q_tile(const VarlenBwdParams& p, Span sq, Span sk, int tile) {
+    return p.causal ? max(tile * BM - (sk.len - sq.len), 0) / BM : 0;
+}
+__device__ __forceinline__ int q_tiles(const VarlenBwdParams& p, Span sq, Span sk, int tile) {
+    return max((sq.len + BM - 1) / BM - first_q_tile(p, sq, sk, tile), 0);
+}
+
 // One warp: zero rows [first, 128) of a tile (two halves of d, a row 128 bytes of each).
 __device__ __forceinline__ void zero_rows(uint32_t tile, int first, int lane) {
     for (int half = 0; half < 2; ++half)
@@ -107,15 +115,14 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
 
     const int warp = warp_id();
     const int lane = lane_id();
-    const int hk = blockIdx.y, group = p.H / p.Hkv;
-    const TileAt at = tile_at(p.cu_k, p.N, p.Tk, BM, blockIdx.x);
-    if (at.seq < 0) return;                               // the grid is an upper bound
-    const Span sq = span_of(p.cu_q, at.seq, p.Tq), sk = span_of(p.cu_k, at.seq, p.Tk);
-    const int kv0 = at.tile * BM;
+    const int hk = blockIdx.x % p.Hkv, group = p.H / p.Hkv;
+    const int2 at = p.order[blockIdx.x / p.Hkv];          // sequence, key tile
+    if (at.x < 0) return;                                 // the grid is an upper bound
+    const Span sq = span_of(p.cu_q, at.x, p.Tq), sk = span_of(p.cu_k, at.x, p.Tk);
+    const int kv0 = at.y * BM;
     const int shift = sk.len - sq.len;                    // causal: query i sees keys 0 .. i + shift
     // Q tiles [i_first, i_first + per_head) of every head of the group; this split's run [it0, it0 + n)
-    const int i_first = p.causal ? max(kv0 - shift, 0) / BM : 0;
-    const int per_head = max((sq.len + BM - 1) / BM - i_first, 0);
+    const int i_first = first_q_tile(p, sq, sk, at.y), per_head = q_tiles(p, sq, sk, at.y);
     const int all = per_head * group;
     const int it0 = static_cast<int>(static_cast<long long>(blockIdx.z) * all / p.splits);
     const int n = static_cast<int>(static_cast<long long>(blockIdx.z + 1) * all / p.splits) - it0;
@@ -523,13 +530,78 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     if (warp == WARP_MMA) tmem_dealloc(tmem, TMEM_COLS);
 }
 
+// One block: p.order[0 .. bound) = the key tiles of all sequences as (sequence, tile), those with most Q
+// tiles first (a counting sort; tiles with equal work in any order), then (-1, 0).
+__device__ void sort_tiles(const VarlenBwdParams& p) {
+    constexpr int BUCKETS = 1024;
+    __shared__ int count[BUCKETS], sums[8], carry;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int b = tid; b < BUCKETS; b += 256) count[b] = 0;
+    if (tid == 0) carry = 0;
+    __syncthreads();
+    // inclusive block scan of one value per thread, on top of what earlier steps summed to
+    auto scan = [&](int v) {
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, v, off);
+            if (lane >= off) v += o;
+        }
+        if (lane == 31) sums[warp] = v;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) v += sums[w];
+        v += carry;
+        __syncthreads();
+        if (tid == 255) carry = v;
+        __syncthreads();
+        return v;
+    };
+    // tile_end[n]: tiles of sequences 0 .. n
+    for (int n0 = 0; n0 < p.N; n0 += 256) {
+        const int n = n0 + tid;
+        const int end = scan(n < p.N ? (span_of(p.cu_k, n, p.Tk).len + BM - 1) / BM : 0);
+        if (n < p.N) p.tile_end[n] = end;
+    }
+    const int total = min(carry, p.tile_bound);              // more only if the offsets are no offsets
+    __syncthreads();
+    auto place = [&](int x, int& seq, int& tile) {           // the first n with tile_end[n] > x
+        int lo = 0, hi = p.N - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (p.tile_end[mid] > x) hi = mid;
+            else lo = mid + 1;
+        }
+        seq = lo;
+        tile = x - (lo ? p.tile_end[lo - 1] : 0);
+        const int work = q_tiles(p, span_of(p.cu_q, lo, p.Tq), span_of(p.cu_k, lo, p.Tk), tile);
+        return BUCKETS - 1 - min(work, BUCKETS - 1);         // bucket 0: the most work
+    };
+    int seq, tile;
+    for (int x = tid; x < total; x += 256) atomicAdd(&count[place(x, seq, tile)], 1);
+    if (tid == 0) carry = 0;
+    __syncthreads();
+    for (int b0 = 0; b0 < BUCKETS; b0 += 256) {              // counts -> first positions
+        const int c = count[b0 + tid], end = scan(c);
+        count[b0 + tid] = end - c;
+    }
+    __syncthreads();
+    for (int x = tid; x < total; x += 256) {
+        const int at = atomicAdd(&count[place(x, seq, tile)], 1);
+        p.order[at] = make_int2(seq, tile);
+    }
+    for (int x = total + tid; x < p.tile_bound; x += 256) p.order[x] = make_int2(-1, 0);
+}
+
 // D_i = sum_d dO_id * O_id (fp32) for every (token, head) row, and dQ accumulator := 0.
-// 16 threads per row, 8 elements (16 bytes) each.
+// 16 threads per row, 8 elements (16 bytes) each.  The first block sorts the key tiles instead.
 __global__ void __launch_bounds__(256) varlen_prep_kernel(const VarlenBwdParams p) {
+    if (blockIdx.x == 0) {
+        sort_tiles(p);
+        return;
+    }
     const long long rows = static_cast<long long>(p.Tq) * p.H, total = rows * 16;
     const int lane = threadIdx.x & 31;
-    const long long warp0 = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x - lane;
-    const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+    const long long warp0 = static_cast<long long>(blockIdx.x - 1) * blockDim.x + threadIdx.x - lane;
+    const long long stride = static_cast<long long>(gridDim.x - 1) * blockDim.x;
     const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o);
     const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(p.dout);
     for (long long t0 = warp0; t0 < total; t0 += stride) {        // warp-uniform trip count
@@ -582,22 +654,34 @@ __global__ void __launch_bounds__(256) varlen_cast_kernel(const float* __restric
     }
 }
 
-static long long tile_bound(int N, int Tk) {
-    const long long bound = Tk / BM + static_cast<long long>(N);
-    return bound < Tk ? bound : Tk;
-}
-
 }  // namespace varlen_bwd
 
-// CTAs among which a key tile's Q tiles are split: where the key tiles alone give fewer than two CTAs
-// per SM, as many as make four, each with at least two Q tiles on average.
+int varlen_bwd_tile_bound(int N, int Tk) {
+    const long long bound = Tk / varlen_bwd::BM + static_cast<long long>(N);
+    return static_cast<int>(bound < Tk ? bound : Tk);
+}
+
+// CTAs among which a key tile's Q tiles are split: the number with the least estimated time, in units of
+// one Q tile's products (3.4 us measured).  Most work first, the CTAs finish together unless one is longer
+// than its SM's share: the larger of the two, with about 3 units of prologue and epilogue for every CTA;
+// some of a CTA for the uneven end; and about 5 units of extra launches to clear and cast the fp32 dK, dV
+// when there is more than one.  From the sizes alone: sequences of average length, full.  One sequence of
+// 2000 and 12 heads takes 70 us unsplit, 106 us in three; one of 4096 with 16 heads over a single kv head
+// 0.32 ms split, 1.54 ms unsplit.
 int varlen_bwd_splits(int N, int Tq, int Tk, int H, int Hkv) {
-    const long long ctas = varlen_bwd::tile_bound(N, Tk) * Hkv;
-    if (ctas == 0 || ctas >= 2 * 148) return 1;
-    const long long q_tiles = (static_cast<long long>(Tq) / N + varlen_bwd::BM - 1) / varlen_bwd::BM * (H / Hkv);
-    long long s = (4 * 148 + ctas - 1) / ctas;
-    if (s > q_tiles / 2) s = q_tiles / 2;
-    return s < 1 ? 1 : s > 64 ? 64 : static_cast<int>(s);
+    const double ctas = static_cast<double>(varlen_bwd_tile_bound(N, Tk)) * Hkv;
+    const double q_tiles = static_cast<double>((static_cast<long long>(Tq) / N + varlen_bwd::BM - 1) / varlen_bwd::BM) * (H / Hkv);
+    int best = 1;
+    double least = 0;
+    for (int s = 1; s <= 64 && s <= q_tiles; ++s) {
+        const double share = ctas * (q_tiles + 3 * s) / 148, one = q_tiles / s + 3;
+        const double time = (share > one ? share : one) + 0.15 * one + (s > 1 ? 5 : 0);
+        if (s == 1 || time < least) {
+            least = time;
+            best = s;
+        }
+    }
+    return best;
 }
 
 int launch_varlen_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
@@ -605,10 +689,8 @@ int launch_varlen_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
                       cudaStream_t stream) {
     using namespace varlen_bwd;
     const int blocks = 148 * 8;          // grid-stride elementwise kernels: 8 blocks of 256 per SM
-    if (p.Tq > 0) {
-        varlen_prep_kernel<<<blocks, 256, 0, stream>>>(p);
-        if (cudaGetLastError() != cudaSuccess) return -1;
-    }
+    varlen_prep_kernel<<<1 + blocks, 256, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return -1;
     if (p.Tk > 0) {
         if (p.splits > 1) {
             const size_t bytes = static_cast<size_t>(p.Tk) * p.Hkv * HD * 4;
@@ -617,7 +699,7 @@ int launch_varlen_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
                 return -1;
         }
         if (configure_smem(reinterpret_cast<const void*>(varlen_main_kernel), SMEM_BYTES) != 0) return -1;
-        const dim3 grid(static_cast<unsigned>(tile_bound(p.N, p.Tk)), p.Hkv, p.splits);
+        const dim3 grid(static_cast<unsigned>(p.tile_bound) * p.Hkv, 1, p.splits);
         varlen_main_kernel<<<grid, NTHREADS, SMEM_BYTES, stream>>>(tq, tk, tv, tdo, tdq, tdk, tdv, p);
         if (cudaGetLastError() != cudaSuccess) return -1;
         if (p.splits > 1) {

@@ -18,7 +18,8 @@ __device__ __forceinline__ Span span_of(const int* cu, int n, int T) {
 // Tile `target` of the tiles that all sequences' rows (on the axis of `cu`) split into, `rows` to a
 // tile and each sequence starting a tile of its own: the sequence and the tile within it, or seq = -1
 // past the last.  The whole warp calls it; 32 sequences a step, so no table has to be built (and no
-// extra launch made) before the attention kernel.
+// extra launch made) before the attention kernel.  Up to 32 sequences are taken longest first, so that
+// the work handed out last is short; more are taken as they come.
 struct TileAt {
     int seq, tile, tiles;          // tiles: of that sequence
 };
@@ -27,19 +28,28 @@ __device__ __forceinline__ TileAt tile_at(const int* cu, int N, int T, int rows,
     int before = 0;
     for (int n0 = 0; n0 < N; n0 += 32) {
         const int mine = n0 + lane < N ? (span_of(cu, n0 + lane, T).len + rows - 1) / rows : 0;
-        int upto = mine;
+        int upto;                                  // tiles up to and including this lane's sequence
+        if (N <= 32) {
+            upto = 0;
+            for (int l = 0; l < N; ++l) {
+                const int o = __shfl_sync(0xffffffffu, mine, l);
+                if (o > mine || (o == mine && l <= lane)) upto += o;
+            }
+        } else {
+            upto = mine;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += o;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += o;
+            }
         }
-        const unsigned past = __ballot_sync(0xffffffffu, before + upto > target);
-        if (past) {
-            const int l = __ffs(past) - 1;
+        const unsigned here = __ballot_sync(0xffffffffu, before + upto > target && before + upto - mine <= target);
+        if (here) {
+            const int l = __ffs(here) - 1;
             const int tiles = __shfl_sync(0xffffffffu, mine, l);
             return {n0 + l, target - before - __shfl_sync(0xffffffffu, upto, l) + tiles, tiles};
         }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+        before += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine));
     }
     return {-1, 0, 0};
 }

@@ -99,6 +99,9 @@ struct VarlenBwdParams : VarlenParams {
     float* dq_acc;                    // workspace fp32 [Tq, H, 128]: unscaled dS K
     float* delta;                     // workspace fp32 [H, Tq]: rowsum(dO * O)
     float *dk_acc, *dv_acc;           // workspace fp32 [Tk, Hkv, 128], splits > 1 only
+    int tile_bound;                   // key tiles, an upper bound
+    int2* order;                      // workspace [tile_bound]: key tiles as (sequence, tile), most work first
+    int* tile_end;                    // workspace [N]: key tiles up to and including each sequence
 };
 
 struct Int8GemmParams {
@@ -161,6 +164,7 @@ int launch_varlen_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
                       const CUtensorMap& tdq, const CUtensorMap& tdk, const CUtensorMap& tdv, const VarlenBwdParams& p,
                       cudaStream_t stream);
 int varlen_bwd_splits(int N, int Tq, int Tk, int H, int Hkv);
+int varlen_bwd_tile_bound(int N, int Tk);
 
 // Int8 linear layer (int8_linear.cu) and its backward (int8_grad.cu).  0 on success.
 int launch_int8_quant_rows(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream);
