@@ -17,8 +17,6 @@ namespace int8 {
 // ------------------------------------------------------------------------------------
 // rows <-> 8 bits
 // ------------------------------------------------------------------------------------
-constexpr int CACHED = 4;          // 8-element pieces of a row that a thread keeps between its two passes
-
 __device__ __forceinline__ float2 bf16x2_floats(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
@@ -42,8 +40,9 @@ __device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, float pre, 
 }
 
 // T threads per row (a power of two, 32 to 256), 256 / T rows per block.  Bound by memory: x is read once
-// (rows of up to 32 T elements stay in registers between the absmax and the codes), the codes written once.
-template <int T>
+// (rows of up to 8 CACHED T elements stay in registers between the absmax and the codes), the codes written
+// once.
+template <int T, int CACHED>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16* __restrict__ x, int8_t* __restrict__ codes,
                                                          float* __restrict__ scales, int M, int K, long long ldx) {
     grid_launch_dependents();                              // a layer's product may fetch its weight meanwhile
@@ -95,22 +94,31 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16* __
     for (int c = CACHED * T + tid; c < pieces; c += T) put(c, row[c]);
 }
 
-// 16 codes per thread and step; K % 16 == 0, so they are of one row.  Bound by memory.
-__global__ void __launch_bounds__(256) dequant_rows_kernel(const uint4* __restrict__ codes, const float* __restrict__ scales,
-                                                           uint4* __restrict__ x, int K16, long long n16) {
-    for (long long t = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; t < n16; t += 256ll * gridDim.x) {
-        const uint4 u = codes[t];
-        const float s = scales[t / K16];
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        uint32_t o[8];
+// T threads per row, 256 / T rows per block, 8 codes per thread and step (a warp's store is 512 bytes in one
+// piece), eight steps' codes in flight.  Bound by memory.
+template <int T>
+__global__ void __launch_bounds__(256) dequant_rows_kernel(const uint2* __restrict__ codes, const float* __restrict__ scales,
+                                                           uint4* __restrict__ x, int M, int K8) {
+    const long long m = static_cast<long long>(blockIdx.x) * (256 / T) + threadIdx.x / T;
+    if (m >= M) return;
+    const float s = scales[m];
+    const uint2* src = codes + m * K8;
+    uint4* dst = x + m * K8;
+    for (int c0 = threadIdx.x % T; c0 < K8; c0 += 8 * T) {
+        uint2 u[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int a = static_cast<int>(w[e]);
-            o[2 * e] = pack_bf16x2(s * static_cast<float>(a << 24 >> 24), s * static_cast<float>(a << 16 >> 24));
-            o[2 * e + 1] = pack_bf16x2(s * static_cast<float>(a << 8 >> 24), s * static_cast<float>(a >> 24));
+        for (int i = 0; i < 8; ++i)
+            if (c0 + i * T < K8) u[i] = src[c0 + i * T];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (c0 + i * T >= K8) break;
+            const int a = static_cast<int>(u[i].x), b = static_cast<int>(u[i].y);
+            dst[c0 + i * T] = make_uint4(
+                pack_bf16x2(s * static_cast<float>(a << 24 >> 24), s * static_cast<float>(a << 16 >> 24)),
+                pack_bf16x2(s * static_cast<float>(a << 8 >> 24), s * static_cast<float>(a >> 24)),
+                pack_bf16x2(s * static_cast<float>(b << 24 >> 24), s * static_cast<float>(b << 16 >> 24)),
+                pack_bf16x2(s * static_cast<float>(b << 8 >> 24), s * static_cast<float>(b >> 24)));
         }
-        x[2 * t] = make_uint4(o[0], o[1], o[2], o[3]);
-        x[2 * t + 1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 
@@ -534,27 +542,36 @@ int launch(const CUtensorMap& tx, const CUtensorMap& tw, const Int8GemmParams& p
 }
 }  // namespace few
 
-template <int T>
+template <int T, int CACHED>
 void launch_quant(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream) {
     const int rows = 256 / T;
-    quant_rows_kernel<T><<<(M + rows - 1) / rows, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(x),
-                                                                    static_cast<int8_t*>(codes), scales, M, K, ldx);
+    quant_rows_kernel<T, CACHED><<<(M + rows - 1) / rows, 256, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(x), static_cast<int8_t*>(codes), scales, M, K, ldx);
+}
+template <int T>
+void launch_dequant(const void* codes, const float* scales, void* x, int M, int K, cudaStream_t stream) {
+    const int rows = 256 / T;
+    dequant_rows_kernel<T><<<(M + rows - 1) / rows, 256, 0, stream>>>(static_cast<const uint2*>(codes), scales,
+                                                                      static_cast<uint4*>(x), M, K / 8);
 }
 
 }  // namespace int8
 
 int launch_int8_quant_rows(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream) {
-    if (K <= 1024) int8::launch_quant<32>(x, codes, scales, M, K, ldx, stream);
-    else if (K <= 2048) int8::launch_quant<64>(x, codes, scales, M, K, ldx, stream);
-    else if (K <= 4096) int8::launch_quant<128>(x, codes, scales, M, K, ldx, stream);
-    else int8::launch_quant<256>(x, codes, scales, M, K, ldx, stream);
+    // few rows: all of a block on each, for latency; else as few threads as keep the row in registers
+    if (M <= 148) int8::launch_quant<256, 4>(x, codes, scales, M, K, ldx, stream);
+    else if (K <= 1024) int8::launch_quant<32, 4>(x, codes, scales, M, K, ldx, stream);
+    else if (K <= 2048) int8::launch_quant<32, 8>(x, codes, scales, M, K, ldx, stream);
+    else if (K <= 4096) int8::launch_quant<64, 8>(x, codes, scales, M, K, ldx, stream);
+    else if (K <= 8192) int8::launch_quant<128, 8>(x, codes, scales, M, K, ldx, stream);
+    else int8::launch_quant<256, 8>(x, codes, scales, M, K, ldx, stream);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 int launch_int8_dequant_rows(const void* codes, const float* scales, void* x, int M, int K, cudaStream_t stream) {
-    const long long n16 = static_cast<long long>(M) * K / 16, blocks = (n16 + 255) / 256;
-    int8::dequant_rows_kernel<<<static_cast<unsigned>(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, stream>>>(
-        static_cast<const uint4*>(codes), scales, static_cast<uint4*>(x), K / 16, n16);
+    if (K <= 2048) int8::launch_dequant<32>(codes, scales, x, M, K, stream);
+    else if (K <= 8192) int8::launch_dequant<64>(codes, scales, x, M, K, stream);
+    else int8::launch_dequant<256>(codes, scales, x, M, K, stream);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 

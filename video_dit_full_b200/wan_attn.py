@@ -345,16 +345,23 @@ def fp8_linear(x, w_codes, w_scale, stream=None):
     return fp8_gemm(codes, scales, w_codes, w_scale, stream=stream)
 
 
+torch = None                       # the module, once a call below has needed it
+
+
+def _need_torch():
+    global torch
+    import torch as module
+    torch = module
+
+
 def _call_stream(stream, device):
     """The stream's handle as an integer; the current stream of `device` if none is given."""
-    import torch
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _same_device(first, **others):
     """The index of the one device that every tensor is on, which must be the current one (the device
     whose context and stream the call uses)."""
-    import torch
     dev = torch.cuda.current_device()
     if first.get_device() != dev:
         raise ValueError(f"the tensors are on {first.device}, the current device is cuda:{dev}")
@@ -366,7 +373,6 @@ def _same_device(first, **others):
 
 def _check_packed(name, t, shape=None):
     """A bf16 [T, H, D] CUDA tensor whose tokens may be strided; returns the token stride in elements."""
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
@@ -388,7 +394,6 @@ def _check_packed(name, t, shape=None):
 
 
 def _check_offsets(name, t):
-    import torch
     _check_plain(name, t, torch.int32)
     if t.dim() != 1 or t.shape[0] < 2:
         raise ValueError(f"{name} must be [sequences + 1]")
@@ -411,7 +416,6 @@ def _check_packed_call(q, k, v, cu_q, cu_k):
 
 def _workspace(need, given, like):
     """(pointer, bytes, tensor to keep) of the given workspace, or of a new one if the call needs any."""
-    import torch
     if given is None:
         if not need:
             return None, 0, None
@@ -428,7 +432,8 @@ def varlen_fwd(q, k, v, cu_q, cu_k, causal=False, o=None, lse=None, workspace=No
     may be strided), sequence n at rows cu_q[n]:cu_q[n+1] and cu_k[n]:cu_k[n+1] (int32, on the device).
 
     Rows of a given o / lse outside every sequence keep what they held; without one they are undefined."""
-    import torch
+    if torch is None:
+        _need_torch()
     N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv = _check_packed_call(q, k, v, cu_q, cu_k)
     if o is None:
         o = q.new_empty((Tq, H, D))
@@ -455,7 +460,8 @@ def varlen_bwd_workspace_size(N, Tq, Tk, H, Hkv, D=128) -> int:
 def varlen_bwd(q, k, v, o, do, lse, cu_q, cu_k, causal=False, dq=None, dk=None, dv=None, workspace=None,
                stream=None):
     """dQ, dK, dV of sum(O * dO) for packed sequences (``wan_attn_varlen_bwd``); given dq, dk, dv may be strided."""
-    import torch
+    if torch is None:
+        _need_torch()
     N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv = _check_packed_call(q, k, v, cu_q, cu_k)
     _check_plain("o", o, torch.bfloat16, Tq * H * D)
     _check_plain("do", do, torch.bfloat16, Tq * H * D)
@@ -489,7 +495,6 @@ def _check_matrix(name, t, dtype, cols=None):
 
 def _check_activations(x):
     """bf16 [M, K] whose rows may be strided; returns M, K and the row stride in elements."""
-    import torch
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.bfloat16:
         raise TypeError("x must be a bfloat16 CUDA tensor")
     if x.dim() != 2:
@@ -508,7 +513,8 @@ def _check_activations(x):
 def int8_quantize_rows(x, codes=None, scales=None, stream=None):
     """int8 codes [M, K] and fp32 scales [M] of bf16 x [M, K], a scale per row (``wan_int8_quantize_rows``):
     an activation's 8-bit checkpoint, or a weight [N, K] with a scale per output channel."""
-    import torch
+    if torch is None:
+        _need_torch()
     M, K, ldx = _check_activations(x)
     codes = x.new_empty((M, K), dtype=torch.int8) if codes is None else codes
     scales = x.new_empty(M, dtype=torch.float32) if scales is None else scales
@@ -522,7 +528,8 @@ def int8_quantize_rows(x, codes=None, scales=None, stream=None):
 
 def int8_dequantize_rows(codes, scales, x=None, stream=None):
     """bf16 [M, K] = codes * scales: an 8-bit checkpoint read back (``wan_int8_dequantize_rows``)."""
-    import torch
+    if torch is None:
+        _need_torch()
     M, K = _check_matrix("codes", codes, torch.int8)
     _check_plain("scales", scales, torch.float32, M)
     x = codes.new_empty((M, K), dtype=torch.bfloat16) if x is None else x
@@ -534,7 +541,6 @@ def int8_dequantize_rows(codes, scales, x=None, stream=None):
 
 
 def _check_weight(w_codes, w_scales, bias, K):
-    import torch
     N, _ = _check_matrix("w_codes", w_codes, torch.int8, K)
     _check_plain("w_scales", w_scales, torch.float32, N)
     if bias is not None:
@@ -544,7 +550,8 @@ def _check_weight(w_codes, w_scales, bias, K):
 
 def int8_gemm(a_codes, a_scales, w_codes, w_scales, bias=None, y=None, stream=None):
     """bf16 Y [M, N] = diag(a_scales) (a_codes w_codes^T) diag(w_scales) + bias through ``wan_int8_gemm``."""
-    import torch
+    if torch is None:
+        _need_torch()
     M, K = _check_matrix("a_codes", a_codes, torch.int8)
     _check_plain("a_scales", a_scales, torch.float32, M)
     N = _check_weight(w_codes, w_scales, bias, K)
@@ -561,24 +568,30 @@ def int8_linear(x, w_codes, w_scales, bias=None, return_checkpoint=False, stream
     """Y = the int8 linear layer of bf16 x [M, K] (rows may be strided) with a weight quantised by
     int8_quantize_rows (``wan_int8_linear``).  With return_checkpoint: (Y, codes, scales), the 8-bit
     codes of x that int8_grad_weight takes in the backward."""
-    import torch
+    if torch is None:
+        _need_torch()
     M, K, ldx = _check_activations(x)
     N = _check_weight(w_codes, w_scales, bias, K)
-    y = x.new_empty((M, N))
-    codes = x.new_empty((M, K), dtype=torch.int8)
-    scales = x.new_empty(M, dtype=torch.float32)
     dev = _same_device(x, w_codes=w_codes, w_scales=w_scales, bias=bias)
+    y = x.new_empty((M, N))
+    if return_checkpoint:
+        codes, scales = x.new_empty((M, K), dtype=torch.int8), x.new_empty(M, dtype=torch.float32)
+        codes_at, scales_at = codes.data_ptr(), scales.data_ptr()
+    else:                                          # scratch: the codes, then the scales (K % 16 == 0)
+        scratch = x.new_empty(M * (K + 4), dtype=torch.uint8)
+        codes_at = scratch.data_ptr()
+        scales_at = codes_at + M * K
     _check("wan_int8_linear", lib().wan_int8_linear(x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
-                                                    None if bias is None else bias.data_ptr(), y.data_ptr(),
-                                                    codes.data_ptr(), scales.data_ptr(), M, N, K, ldx,
-                                                    _call_stream(stream, dev)))
+                                                    None if bias is None else bias.data_ptr(), y.data_ptr(), codes_at,
+                                                    scales_at, M, N, K, ldx, _call_stream(stream, dev)))
     return (y, codes, scales) if return_checkpoint else y
 
 
 def int8_grad_weight(dy, codes, scales, dw=None, stream=None):
     """bf16 dW [N, K] = dY^T (codes * scales) from dY [M, N] and the layer input's 8-bit checkpoint
     (``wan_int8_grad_weight``)."""
-    import torch
+    if torch is None:
+        _need_torch()
     M, N = _check_matrix("dy", dy, torch.bfloat16)
     rows, K = _check_matrix("codes", codes, torch.int8)
     if rows != M:
@@ -595,7 +608,8 @@ def int8_grad_weight(dy, codes, scales, dw=None, stream=None):
 def int8_grad_input(dy, w_codes, w_scales, dx=None, stream=None):
     """bf16 dX [M, K] = dY (w_codes * w_scales) from dY [M, N] and the weight's 8-bit codes
     (``wan_int8_grad_input``)."""
-    import torch
+    if torch is None:
+        _need_torch()
     M, N = _check_matrix("dy", dy, torch.bfloat16)
     rows, K = _check_matrix("w_codes", w_codes, torch.int8)
     if rows != N:
