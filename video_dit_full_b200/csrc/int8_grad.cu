@@ -463,10 +463,10 @@ int launch(const CUtensorMap& ta, const CUtensorMap& tc, const Params& p, cudaSt
         return cudaGetLastError() == cudaSuccess ? 0 : -1;
     }
     if (configure_smem(reinterpret_cast<const void*>(grad_split_kernel<A_MN>), SMEM_BYTES) != 0) return -1;
-    // the terms are split while that still fits one CTA per SM and each has four stages or more
+    // the terms are split while that still fits one CTA per SM and each has eight stages or more
     const int nk = (p.terms + BT - 1) / BT;
     int splits = 1;
-    while (splits < 8 && 2 * splits * t128 <= 148 && nk / (2 * splits) >= 4) splits *= 2;
+    while (splits < 8 && (splits + 1) * t128 <= 148 && nk / (splits + 1) >= 8) ++splits;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(splits, static_cast<unsigned>(t128 < 65535 ? t128 : 65535), static_cast<unsigned>((t128 + 65534) / 65535));
     cfg.blockDim = dim3(NTHREADS);
