@@ -3,17 +3,23 @@
 // with a(t, r) = dY[t, r] for dW (t = tokens; the codes are the activation's checkpoint) and
 // a(t, r) = dY[r, t] for dX (t = output channels; the codes are the weight's).
 //
-// Bound by the bf16 tensor cores.  The codes stay 8 bits until they are in shared memory: TMA brings
-// [64 t][128 c] bytes, converter warps multiply by the row's scale in fp32 and write bf16 into the
-// swizzled layout that the MMA reads, so the dequantised matrix never exists in memory (a pass of its
-// own would write and read 4 bytes for every code).  The one rounding on the way, x to bf16 (2^-8
-// relative at most), is what the tensor core's operand type costs; dY is used as it is, sums are fp32.
-// Byte to float costs one PRMT and half an add: the code + 128 goes under the exponent of 2^23.
+// Bound by the bf16 tensor cores.  The codes stay 8 bits until they are on the SM: TMA brings
+// [64 t][128 c] bytes, converter warps multiply by the row's scale in fp32 and write bf16 into tensor
+// memory, so the dequantised matrix never exists in memory (a pass of its own would write and read 4 bytes
+// for every code).  The one rounding on the way, x to bf16 (2^-8 relative at most), is what the tensor
+// core's operand type costs; dY is used as it is, sums are fp32.  Byte to float costs one PRMT and half an
+// add: the code + 128 goes under the exponent of 2^23.
 //
-// Two launches of the same roles (warp 0 TMA of A, 1 MMA, 2-5 epilogue, 6-13 converters, 14 TMA of the codes; a stage holds A, the
-// codes and their bf16 form, 16 + 8 + 16 KB):
-//   PAIR   persistent CTA pairs (cta_group::2) on 256 x 256 tiles: each CTA converts its 128 columns of
-//          the pair's 256, half of what a CTA alone would have to for the same number of products
+// The MMA's rows (TMEM lanes) are c and its columns r: x, transposed, is the operand that tensor memory can
+// hold.  ldmatrix with transposition gives a thread four consecutive t of one c, and the 16x256b store takes
+// them in exactly that fragment.  With x converted into a shared-memory operand instead, writing it and the
+// MMA reading it back added 32 KB of shared-memory traffic to a stage's 56, past the 64 KB that the products
+// leave time for: 1070 TFLOP/s.
+//
+// Two launches of the same roles (warp 0 TMA of dY, 1 MMA, 2-5 epilogue, 6-13 converters, 14 TMA of the
+// codes; a stage holds dY and the codes, 16 + 8 KB, and its x 32 columns of TMEM):
+//   PAIR   persistent CTA pairs (cta_group::2) on 256 x 256 tiles: each CTA converts its 128 c and loads
+//          its 128 r of the pair's
 //   else   one 128 x 128 tile per CTA; a cluster splits t and joins its fp32 partial tiles in rank order
 //          (deterministic) through distributed shared memory: sizes whose 256 x 256 tiles leave SMs idle
 #include <cuda.h>
@@ -25,25 +31,28 @@ namespace wan {
 namespace int8_grad {
 
 constexpr int BT = 64;                                       // terms of the sum per stage
-constexpr int STAGES = 5;
-constexpr int A_BYTES = 128 * BT * 2, C_BYTES = 128 * BT, B_BYTES = 128 * BT * 2;
-constexpr int HALF_BYTES = B_BYTES / 2;                      // 64 columns of an MN-major tile
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES + C_BYTES;     // A | B | codes
+constexpr int STAGES = 8;
+constexpr int Y_BYTES = 128 * BT * 2, C_BYTES = 128 * BT;    // dY | codes
+constexpr int HALF_BYTES = Y_BYTES / 2;                      // 64 columns of an MN-major tile
+constexpr int STAGE_BYTES = Y_BYTES + C_BYTES;
+constexpr int X_COLS = BT / 2;                               // TMEM columns of a stage's x (bf16 pairs)
 constexpr int OFF_BAR = STAGES * STAGE_BYTES;
-enum Bar { FULL = 0, CODES = STAGES, READY = 2 * STAGES, EMPTY = 3 * STAGES, TFULL = 4 * STAGES, TEMPTY = 4 * STAGES + 2,
-           DRAIN = 4 * STAGES + 4, NBARS = 4 * STAGES + 5 };
+enum Bar { FULL = 0, CODES = STAGES, READY = 2 * STAGES, EMPTY = 3 * STAGES, TFULL = 4 * STAGES, TEMPTY = 4 * STAGES + 1,
+           DRAIN = 4 * STAGES + 2, NBARS = 4 * STAGES + 3 };
 constexpr int OFF_TMEM_SLOT = OFF_BAR + NBARS * 8;
 constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
 constexpr int OFF_EPI = (OFF_ABORT + 8 + 15) & ~15;          // per epilogue warp: 32 rows x 64 B
 constexpr int EPI_WARP_BYTES = 32 * 64;
 constexpr int GROUPS = 2;                                    // of four converter warps
 constexpr int WARP_CODES = 6 + 4 * GROUPS, NTHREADS = (WARP_CODES + 1) * 32;
-constexpr int SCALE_AHEAD = 4, SCALE_WARP_BYTES = SCALE_AHEAD * 64;         // per converter warp: 16 scales a stage
+constexpr int SCALE_AHEAD = 3, SCALE_WARP_BYTES = SCALE_AHEAD * BT * 4;     // per converter warp: a stage's scales
 constexpr int OFF_SCALES = OFF_EPI + 4 * EPI_WARP_BYTES;
 constexpr int SMEM_BYTES = OFF_SCALES + 4 * GROUPS * SCALE_WARP_BYTES + 1024;
 constexpr int GROUP = 16;                                    // tile order: row blocks in groups
+constexpr uint32_t TMEM_COLS = 512;                          // an fp32 tile, then the stages' x
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 static_assert(128 * 128 * 4 <= STAGES * STAGE_BYTES, "a partial tile reuses the stages");
+static_assert(256 + STAGES * X_COLS <= TMEM_COLS, "tile and stages in TMEM");
 
 struct Params {
     const float* scales;              // fp32 [terms]
@@ -53,12 +62,31 @@ struct Params {
     int* status;
 };
 
-__device__ __forceinline__ void mma_f16_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void mma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                                 uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Two 16 x 16 byte matrices, transposed: lane L's address is row L % 16 of matrix L / 16; it gets columns
+// L / 4 and L / 4 + 8 of each, rows 4 (L % 4) .. + 3, one register each.
+__device__ __forceinline__ void ldmatrix_t8_x2(uint32_t addr, uint32_t (&v)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 16 lanes x 32 columns: registers 4k .. 4k + 3 are columns 8k + 2 (L % 4), + 1 of lane L / 4, then of lane
+// L / 4 + 8.
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 
@@ -98,10 +126,9 @@ __device__ __forceinline__ uint32_t scale2(uint32_t w, float2 s) {
     return pack_bf16x2(x.x, x.y);
 }
 
-template <bool A_MN, bool PAIR>
-__device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtensorMap& tma_c, const Params& p) {
+template <bool Y_MN, bool PAIR>
+__device__ __forceinline__ void grad_body(const CUtensorMap& tma_y, const CUtensorMap& tma_c, const Params& p) {
     constexpr int CG = PAIR ? 2 : 1, TILE = 128 * CG;
-    constexpr uint32_t TMEM_COLS = 2 * TILE;                 // two fp32 accumulators
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;       // the same offset in every CTA
@@ -132,7 +159,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
         const long long w = t - g * per_group;
         r0 = (g * GROUP + static_cast<int>(w % rows)) * TILE;
         c0 = static_cast<int>(w / rows) * TILE;
-        if (PAIR) {                                          // this CTA's rows of A and columns of B
+        if (PAIR) {                                          // this CTA's r of dY and c of the codes
             r0 += rank * 128;
             c0 += rank * 128;
         }
@@ -145,10 +172,8 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
             mbar_init(bar(READY + s), 4 * CG);
             mbar_init(bar(EMPTY + s), 1);
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(bar(TFULL + b), 1);
-            mbar_init(bar(TEMPTY + b), 128 * CG);
-        }
+        mbar_init(bar(TFULL), 1);
+        mbar_init(bar(TEMPTY), 128 * CG);
         mbar_init(bar(DRAIN), 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -171,9 +196,9 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
 
     if (warp == 0) {
-        // ------------------------------ TMA producer of A -------------------------
+        // ------------------------------ TMA producer of dY ------------------------
         if (lane == 0) {
-            tma_prefetch_desc(&tma_a);
+            tma_prefetch_desc(&tma_y);
             const uint32_t full0 = PAIR ? mapa_shared(bar(FULL), 0) : bar(FULL);
             Ring<STAGES> ring;
             uint32_t issued = 0;                             // stages whose copies may be in flight
@@ -186,20 +211,20 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
                     ok = wait_thread(bar(EMPTY + ring.s), ring.use ^ 1u, wc);
                     if (!ok) break;
                     const uint32_t st = base + ring.s * STAGE_BYTES, full = full0 + 8u * ring.s;
-                    if (leader) mbar_arrive_expect_tx(bar(FULL + ring.s), CG * A_BYTES);
+                    if (leader) mbar_arrive_expect_tx(bar(FULL + ring.s), CG * Y_BYTES);
                     // [64 t][2 x 64 r] (dW, MN-major) or [128 r][64 t] (dX, K-major)
                     if (PAIR) {
-                        if (A_MN) {
-                            tma_load_2d_pair(st, &tma_a, full, r0, t0);
-                            tma_load_2d_pair(st + HALF_BYTES, &tma_a, full, r0 + 64, t0);
+                        if (Y_MN) {
+                            tma_load_2d_pair(st, &tma_y, full, r0, t0);
+                            tma_load_2d_pair(st + HALF_BYTES, &tma_y, full, r0 + 64, t0);
                         } else {
-                            tma_load_2d_pair(st, &tma_a, full, t0, r0);
+                            tma_load_2d_pair(st, &tma_y, full, t0, r0);
                         }
-                    } else if (A_MN) {
-                        tma_load_2d(st, &tma_a, full, r0, t0);
-                        tma_load_2d(st + HALF_BYTES, &tma_a, full, r0 + 64, t0);
+                    } else if (Y_MN) {
+                        tma_load_2d(st, &tma_y, full, r0, t0);
+                        tma_load_2d(st + HALF_BYTES, &tma_y, full, r0 + 64, t0);
                     } else {
-                        tma_load_2d(st, &tma_a, full, t0, r0);
+                        tma_load_2d(st, &tma_y, full, t0, r0);
                     }
                     issued = min(issued + 1u, static_cast<uint32_t>(STAGES));
                 }
@@ -221,7 +246,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
                     ok = wait_thread(bar(EMPTY + ring.s), ring.use ^ 1u, wc);
                     if (!ok) break;
                     mbar_arrive_expect_tx(bar(CODES + ring.s), C_BYTES);
-                    tma_load_2d(base + ring.s * STAGE_BYTES + A_BYTES + B_BYTES, &tma_c, bar(CODES + ring.s), c0, t0);
+                    tma_load_2d(base + ring.s * STAGE_BYTES + Y_BYTES, &tma_c, bar(CODES + ring.s), c0, t0);
                     issued = min(issued + 1u, static_cast<uint32_t>(STAGES));
                 }
             }
@@ -230,43 +255,39 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
     } else if (warp == 1) {
         // ------------------------------ MMA issuer (a pair's leader) --------------
         if (lane == 0 && leader) {
-            const uint32_t idesc = make_idesc(1, 1, 1, A_MN ? 1 : 0, 1, TILE, TILE);
+            const uint32_t idesc = make_idesc(1, 1, 1, 0, Y_MN ? 1 : 0, TILE, TILE);
             // K-major: 16 terms are 32 bytes of a row; MN-major: 16 rows of 128 bytes, halves of the other
             // axis HALF_BYTES apart.  The descriptors' high halves are the same, the low ones count 16 bytes.
-            constexpr uint32_t A_STEP = A_MN ? 128 : 2, B_STEP = 128;
-            const uint32_t hi = sdesc_hi();
-            const uint32_t a_lo = sdesc_lo(base, A_MN ? HALF_BYTES : 16), b_lo = sdesc_lo(base + A_BYTES, HALF_BYTES);
-            auto desc = [&](uint32_t lo) { return static_cast<uint64_t>(hi) << 32 | lo; };
+            constexpr uint32_t Y_STEP = Y_MN ? 128 : 2;
+            const uint32_t hi = sdesc_hi(), y_lo = sdesc_lo(base, Y_MN ? HALF_BYTES : 16);
             Ring<STAGES> ring;
             int tc = 0;
             bool ok = true;
             for (long long t = first; t < tiles && ok; t += step, ++tc) {
-                const int b = tc & 1;
-                ok = wait_thread(bar(TEMPTY + b), ((tc >> 1) & 1) ^ 1, wc);
+                ok = wait_thread(bar(TEMPTY), (tc & 1) ^ 1, wc);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + b * TILE;
                 for (int kb = 0; kb < nk; ++kb, ring.next()) {
-                    const uint32_t st = ring.s * (STAGE_BYTES >> 4);
                     ok = wait_thread(bar(FULL + ring.s), ring.use, wc);
                     if (ok)
                         ok = PAIR ? wait_thread_cluster(bar(READY + ring.s), ring.use, wc)
                                   : wait_thread(bar(READY + ring.s), ring.use, wc);
                     if (!ok) break;
                     tc_fence_after();
+                    const uint32_t x = tmem + TILE + ring.s * X_COLS, y = y_lo + ring.s * (STAGE_BYTES >> 4);
 #pragma unroll
                     for (int kk = 0; kk < BT / 16; ++kk) {
-                        const uint64_t a = desc(a_lo + st + kk * A_STEP), bd = desc(b_lo + st + kk * B_STEP);
+                        const uint64_t yd = static_cast<uint64_t>(hi) << 32 | (y + kk * Y_STEP);
                         const uint32_t accumulate = (kb > 0 || kk > 0) ? 1u : 0u;
-                        if (PAIR) mma_f16_ss_pair(acc, a, bd, idesc, accumulate);
-                        else mma_f16_ss(acc, a, bd, idesc, accumulate);
+                        if (PAIR) mma_f16_ts_pair(tmem, x + kk * 8, yd, idesc, accumulate);
+                        else mma_f16_ts(tmem, x + kk * 8, yd, idesc, accumulate);
                     }
                     if (PAIR) mma_commit_pair_both(bar(EMPTY + ring.s));     // both CTAs' stage is free
                     else mma_commit(bar(EMPTY + ring.s));
                 }
                 if (!ok) break;
-                if (PAIR) mma_commit_pair_both(bar(TFULL + b));
-                else mma_commit(bar(TFULL + b));
+                if (PAIR) mma_commit_pair_both(bar(TFULL));
+                else mma_commit(bar(TFULL));
             }
             if (PAIR) mma_commit_pair(bar(DRAIN));
             else mma_commit(bar(DRAIN));
@@ -274,22 +295,23 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
         }
     } else if (warp >= 6) {
         // ------------------------------ converters --------------------------------
-        // Groups of four warps take the stages in turn.  Warp w of a group takes terms 16w .. 16w + 15 of a
-        // stage, four at a time: eight lanes read a term's 128 codes (16 each) and write them as two 16-byte
-        // chunks of its swizzled bf16 row.  The terms' scales come SCALE_AHEAD stages early by cp.async.
-        const int cw = warp - 6, w = cw & 3, sub = lane >> 3, ch = lane & 7;
-        const uint32_t odd = ch >> 2;                        // lanes 4-7 (the other half) write their chunks in
-        const uint32_t ready = PAIR ? mapa_shared(bar(READY), 0) : bar(READY);   // reverse: no bank conflicts
+        // Groups of four warps take the stages in turn.  A warp takes the 32 c of its TMEM quadrant: two times
+        // 16 c, each 64 t as four transposed 16 x 16 matrices.  The codes' rows lie in the 128-byte swizzle, so
+        // that eight of them fall on different banks.  The scales come SCALE_AHEAD stages early by cp.async.
+        const int cw = warp - 6, quad = warp & 3;
+        const uint32_t ready = PAIR ? mapa_shared(bar(READY), 0) : bar(READY);
         const uint32_t ring = base + OFF_SCALES + cw * SCALE_WARP_BYTES;
         const long long total = ((tiles - first + step - 1) / step) * nk;
         auto fetch_scales = [&](long long it, int kb, int slot) {
-            if (it < total && lane < 16) {
-                const int t = (k0 + kb) * BT + w * 16 + lane;
-                const float* src = p.scales + min(t, p.terms - 1);
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ring + slot * 64 + lane * 4), "l"(src),
-                             "r"(t < p.terms ? 4 : 0)        // zero behind the last term
-                             : "memory");
-            }
+            if (it < total)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = (k0 + kb) * BT + e * 32 + lane;
+                    const float* src = p.scales + min(t, p.terms - 1);
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ring + (slot * BT + e * 32 + lane) * 4),
+                                 "l"(src), "r"(t < p.terms ? 4 : 0)          // zero behind the last term
+                                 : "memory");
+                }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         auto after = [&](int kb) { return kb + GROUPS < nk ? kb + GROUPS : (kb + GROUPS) % nk; };
@@ -304,28 +326,30 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
             asm volatile("cp.async.wait_group %0;" ::"n"(SCALE_AHEAD - 1) : "memory");
             if (!wait_warp(bar(CODES + s), stage.use, wc)) break;
             __syncwarp();                                    // every lane's copies are there for every lane
-            const uint32_t sb = base + s * STAGE_BYTES + A_BYTES;
-            const uint8_t* src = smem + s * STAGE_BYTES + A_BYTES + B_BYTES;
-            const float* sc = reinterpret_cast<const float*>(smem + OFF_SCALES + cw * SCALE_WARP_BYTES + slot * 64);
+            const float4* sc = reinterpret_cast<const float4*>(smem + OFF_SCALES + cw * SCALE_WARP_BYTES + slot * BT * 4);
+            const uint32_t codes = base + s * STAGE_BYTES + Y_BYTES;
+            float4 s4[4];                                    // of terms 16 tb + 4 (lane % 4) .. + 3
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int row = w * 16 + q * 4 + sub;
-                const uint4 u = *reinterpret_cast<const uint4*>(src + row * 128 + ch * 16);
-                const uint32_t x[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
-                const float2 s2 = make_float2(sc[q * 4 + sub], sc[q * 4 + sub]);
-                uint32_t o[8];
+            for (int tb = 0; tb < 4; ++tb) s4[tb] = sc[tb * 4 + (lane & 3)];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[2 * e] = scale2<0x7540, 0x7541>(x[e], s2);
-                    o[2 * e + 1] = scale2<0x7542, 0x7543>(x[e], s2);
+            for (int cg = 0; cg < 2; ++cg) {
+                uint32_t x[16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[4];
+                    ldmatrix_t8_x2(sw128_chunk(codes, h * 32 + lane, quad * 2 + cg), v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {            // matrix e / 2, columns lane / 4 (e even) or + 8
+                        const uint32_t w = v[e] ^ 0x80808080u;
+                        const float4 f = s4[h * 2 + (e >> 1)];
+                        x[(h * 2 + (e >> 1)) * 4 + (e & 1) * 2] = scale2<0x7540, 0x7541>(w, make_float2(f.x, f.y));
+                        x[(h * 2 + (e >> 1)) * 4 + (e & 1) * 2 + 1] = scale2<0x7542, 0x7543>(w, make_float2(f.z, f.w));
+                    }
                 }
-                const uint32_t half = sb + (ch >> 2) * HALF_BYTES;
-                const int c0 = (ch & 3) * 2;
-                const uint32_t a0 = sw128_chunk(half, row, c0 + odd), a1 = sw128_chunk(half, row, c0 + 1 - odd);
-                st_shared_v4(a0, odd ? o[4] : o[0], odd ? o[5] : o[1], odd ? o[6] : o[2], odd ? o[7] : o[3]);
-                st_shared_v4(a1, odd ? o[0] : o[4], odd ? o[1] : o[5], odd ? o[2] : o[6], odd ? o[3] : o[7]);
+                tmem_st_16x256b_x4(tmem + TILE + s * X_COLS + (static_cast<uint32_t>(quad * 32 + cg * 16) << 16), x);
             }
-            fence_proxy_async_smem();
+            tmem_wait_st();
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 if (PAIR) mbar_arrive_cluster_relaxed_scope(ready + 8u * static_cast<uint32_t>(s));
@@ -339,61 +363,55 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (PAIR || splits == 1) {
-        // ------------------------------ epilogue: this CTA's 128 rows -------------
+        // ------------------------------ epilogue: this CTA's 128 columns of out ----
+        // TMEM lane = c, column = r.  A warp's 32 c by 32 r at a time go through its 2 KB of shared memory,
+        // [r][c] as bf16, and leave as 64-byte pieces of 32 rows.
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tempty = PAIR ? mapa_shared(bar(TEMPTY), 0) : bar(TEMPTY);
+        const uint32_t wbuf = base + OFF_EPI + (warp - 2) * EPI_WARP_BYTES;
         int tc = 0;
-        bool ok = true;
-        for (long long t = first; t < tiles && ok; t += step, ++tc) {
+        for (long long t = first; t < tiles; t += step, ++tc) {
             int r0, c0;
             tile_of(t, r0, c0);
-            if (PAIR) c0 -= rank * 128;                      // the accumulator spans the pair's columns
-            const int b = tc & 1;
-            ok = wait_warp(bar(TFULL + b), (tc >> 1) & 1, wc);
-            if (!ok) break;
+            if (PAIR) r0 -= rank * 128;                      // the accumulator spans the pair's r
+            if (!wait_warp(bar(TFULL), tc & 1, wc)) break;
             tc_fence_after();
-            // each 32-column chunk goes through the warp's 2 KB of shared memory (16-byte pieces
-            // swizzled by row / 2), so that a store writes 8 whole 64-byte row segments
-            uint8_t* wbuf = smem + OFF_EPI + (warp - 2) * EPI_WARP_BYTES;
-            const int row0 = r0 + (warp & 3) * 32;
+            const int col = c0 + (warp & 3) * 32 + (lane & 3) * 8;
 #pragma unroll 1
             for (int c = 0; c < TILE / 32; ++c) {
+                if (r0 + c * 32 >= p.rows) break;
                 uint32_t v[32];
-                tmem_ld32(tmem + b * TILE + lane_off + c * 32, v);
+                tmem_ld32(tmem + lane_off + c * 32, v);
                 tmem_wait_ld();
-                if (c0 + c * 32 >= p.cols) continue;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[e] = pack_bf16x2(__uint_as_float(v[q * 8 + 2 * e]), __uint_as_float(v[q * 8 + 2 * e + 1]));
-                    *reinterpret_cast<uint4*>(wbuf + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
+                for (int e = 0; e < 32; e += 2) {
+                    const uint32_t two = pack_bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(wbuf + e * 64 + lane * 2), "h"(static_cast<uint16_t>(two))
+                                 : "memory");
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(wbuf + (e + 1) * 64 + lane * 2),
+                                 "h"(static_cast<uint16_t>(two >> 16))
+                                 : "memory");
                 }
                 __syncwarp();
-                const int col = c0 + c * 32 + (lane & 3) * 8;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int rr = 8 * k + (lane >> 2);
-                    const uint4 val =
-                        *reinterpret_cast<const uint4*>(wbuf + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) * 16));
-                    if (row0 + rr < p.rows && col < p.cols)  // cols % 16 == 0
-                        *reinterpret_cast<uint4*>(p.out + static_cast<long long>(row0 + rr) * p.cols + col) = val;
+                    const int rr = 8 * k + (lane >> 2), row = r0 + c * 32 + rr;
+                    const uint4 val = *reinterpret_cast<const uint4*>(smem + (wbuf - base) + rr * 64 + (lane & 3) * 16);
+                    if (row < p.rows && col < p.cols)        // cols % 16 == 0
+                        *reinterpret_cast<uint4*>(p.out + static_cast<long long>(row) * p.cols + col) = val;
                 }
                 __syncwarp();
             }
             tc_fence_before();
-            if (PAIR) mbar_arrive_cluster(tempty + 8u * static_cast<uint32_t>(b));
-            else mbar_arrive(tempty + 8u * static_cast<uint32_t>(b));
+            if (PAIR) mbar_arrive_cluster(tempty);
+            else mbar_arrive(tempty);
         }
     } else {
         // ------------------------------ split: partial tile to shared memory ------
-        // [row][column] fp32 over the stages (every copy has landed and every MMA has read them), columns
-        // rotated by the row in 16-byte pieces: 32 rows of a column piece then fall on different banks
+        // [r][c] fp32 over the stages (every copy has landed and every MMA has read them)
         if (wait_warp(bar(TFULL), 0, wc)) {
             tc_fence_after();
-            const int row = (warp & 3) * 32 + lane;
+            const uint32_t at = base + ((warp & 3) * 32 + lane) * 4;
             const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -401,9 +419,8 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
                 tmem_ld32(src + c * 32, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    st_shared_v4(base + row * 512 + (((c * 8 + q + row) & 31) << 4), v[4 * q], v[4 * q + 1], v[4 * q + 2],
-                                 v[4 * q + 3]);
+                for (int e = 0; e < 32; ++e)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + (c * 32 + e) * 512), "r"(v[e]) : "memory");
             }
         }
     }
@@ -419,7 +436,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
         const int rows = min(128, p.rows - r0), col = c0 + lane * 4;
         if (!*abort_flag && col < p.cols)
             for (int r = rank + warp * splits; r < rows; r += (NTHREADS / 32) * splits) {
-                const uint32_t at = base + r * 512 + (((lane + r) & 31) << 4);
+                const uint32_t at = base + r * 512 + lane * 16;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (int z = 0; z < splits; ++z) {
                     const uint4 v = ld_shared_cluster_v4(mapa_shared(at, z));
@@ -440,29 +457,29 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_a, const CUtens
     }
 }
 
-template <bool A_MN>
+template <bool Y_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
-grad_pair_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_c, const Params p) {
-    grad_body<A_MN, true>(tma_a, tma_c, p);
+grad_pair_kernel(const __grid_constant__ CUtensorMap tma_y, const __grid_constant__ CUtensorMap tma_c, const Params p) {
+    grad_body<Y_MN, true>(tma_y, tma_c, p);
 }
-template <bool A_MN>
+template <bool Y_MN>
 __global__ void __launch_bounds__(NTHREADS, 1)
-grad_split_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_c, const Params p) {
-    grad_body<A_MN, false>(tma_a, tma_c, p);
+grad_split_kernel(const __grid_constant__ CUtensorMap tma_y, const __grid_constant__ CUtensorMap tma_c, const Params p) {
+    grad_body<Y_MN, false>(tma_y, tma_c, p);
 }
 
-template <bool A_MN>
+template <bool Y_MN>
 int launch(const CUtensorMap& ta, const CUtensorMap& tc, const Params& p, cudaStream_t stream) {
     auto tiles = [&](long long n) { return ((p.rows + n - 1) / n) * ((p.cols + n - 1) / n); };
     const long long t256 = tiles(256), t128 = tiles(128);
     // time in 256 x 256 tiles of a pair: a 128 x 128 tile takes a CTA half of one, at 70 % of the rate (it
     // reads twice the shared memory per product)
     if (static_cast<double>((t256 + 73) / 74) <= 0.5 / 0.7 * static_cast<double>((t128 + 147) / 148)) {
-        if (configure_smem(reinterpret_cast<const void*>(grad_pair_kernel<A_MN>), SMEM_BYTES) != 0) return -1;
-        grad_pair_kernel<A_MN><<<2 * static_cast<unsigned>(t256 < 74 ? t256 : 74), NTHREADS, SMEM_BYTES, stream>>>(ta, tc, p);
+        if (configure_smem(reinterpret_cast<const void*>(grad_pair_kernel<Y_MN>), SMEM_BYTES) != 0) return -1;
+        grad_pair_kernel<Y_MN><<<2 * static_cast<unsigned>(t256 < 74 ? t256 : 74), NTHREADS, SMEM_BYTES, stream>>>(ta, tc, p);
         return cudaGetLastError() == cudaSuccess ? 0 : -1;
     }
-    if (configure_smem(reinterpret_cast<const void*>(grad_split_kernel<A_MN>), SMEM_BYTES) != 0) return -1;
+    if (configure_smem(reinterpret_cast<const void*>(grad_split_kernel<Y_MN>), SMEM_BYTES) != 0) return -1;
     // the terms are split while that still fits one CTA per SM and each has eight stages or more
     const int nk = (p.terms + BT - 1) / BT;
     int splits = 1;
@@ -479,7 +496,7 @@ int launch(const CUtensorMap& ta, const CUtensorMap& tc, const Params& p, cudaSt
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, grad_split_kernel<A_MN>, ta, tc, p) == cudaSuccess ? 0 : -1;
+    return cudaLaunchKernelEx(&cfg, grad_split_kernel<Y_MN>, ta, tc, p) == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace int8_grad

@@ -174,7 +174,7 @@ int int8_gemm_token_tile(int M, int N);
 // tx: x's codes, boxes of the token tile's rows (128 for pairs); tw: the weight's codes, boxes of 128 rows.
 int launch_int8_gemm(const CUtensorMap& tx, const CUtensorMap& tw, const Int8GemmParams& p, cudaStream_t stream);
 // out[r, c] = sum_t a(t, r) scales[t] codes[t, c].  weight: a(t, r) = dy[t, r] (rows = N, terms = M), tdy with
-// boxes of (64, 64); else a(t, r) = dy[r, t] (rows = M, terms = N), boxes (64, 128).  tcodes: boxes (128, 64), not swizzled.
+// boxes of (64, 64); else a(t, r) = dy[r, t] (rows = M, terms = N), boxes (64, 128).  tcodes: boxes (128, 64).
 int launch_int8_grad(const CUtensorMap& tdy, const CUtensorMap& tcodes, const float* scales, void* out, int rows, int cols,
                      int terms, bool weight, unsigned long long budget_ns, int* status, cudaStream_t stream);
 
