@@ -90,6 +90,28 @@ __device__ __forceinline__ int fresh(int v) {
     return v;
 }
 
+// The scheduler's waits last as long as an item does (milliseconds for a million keys), unlike all others:
+// it gives up when another role has (the abort flag), and by itself only after 64 budgets.
+__device__ __forceinline__ bool wait_item(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (it & 15u) continue;
+        int stop = 0;
+        if ((threadIdx.x & 31) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            stop = *w.abort_flag;
+            if (!stop && (now - t0) / 64 > w.budget_ns) {
+                *w.abort_flag = 1;
+                report_status(w.status, kStatusTimeout);
+                stop = 1;
+            }
+        }
+        if (__shfl_sync(0xffffffffu, stop, 0)) return false;
+    }
+}
+
 __global__ void __launch_bounds__(NTHREADS, 1)
 varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
@@ -150,9 +172,10 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         const int packed_heads = p.H / p.pack;
         int x = blockIdx.x, z = blockIdx.y;
         uint32_t asked = 0, item = 0;
+        ScanFrom from;
         bool more = true, pending = false;
         while (more) {
-            const TileAt at = tile_at(p.cu_q, p.N, p.Tq, 2 * tile_tokens, x / packed_heads);
+            const TileAt at = tile_at(p.cu_q, p.N, p.Tq, 2 * tile_tokens, x / packed_heads, from);
             if (at.seq >= 0) {                        // the grid is an upper bound
                 const Span sq = span_of(p.cu_q, at.seq, p.Tq), sk = span_of(p.cu_k, at.seq, p.Tk);
                 const int i0 = (at.tiles - 1 - at.tile) * 2 * tile_tokens;
@@ -169,7 +192,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                 const int share = (all + p.splits - 1) / p.splits;
                 const int j0 = min(z * share, all);
                 const int n = min(share, all - j0);   // blocks j0 .. j0 + n - 1
-                if (!wait_warp(bar(W_EMPTY + (item & 1u)), ((item >> 1) & 1u) ^ 1u, wc)) break;
+                if (!wait_item(bar(W_EMPTY + (item & 1u)), ((item >> 1) & 1u) ^ 1u, wc)) break;
                 if (lane == 0) {
                     volatile Work* w = slot_of(item);
                     const bool shared = i0 + tile_tokens >= sq.len && n > 1;
@@ -189,7 +212,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                 }
                 // the producer says when this item nears its end: a block taken earlier could wait here while
                 // other SMs run out of work
-                if (!wait_warp(bar(NEXT), item & 1u, wc)) break;
+                if (!wait_item(bar(NEXT), item & 1u, wc)) break;
                 ++item;
             }
             pending = true;
@@ -206,7 +229,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
             __syncwarp();
         }
         if (pending) drain_wait(bar(CLC), asked & 1u);    // the answer must not land in memory that is gone
-        if (!*abort_flag && wait_warp(bar(W_EMPTY + (item & 1u)), ((item >> 1) & 1u) ^ 1u, wc) && lane == 0) {
+        if (!*abort_flag && wait_item(bar(W_EMPTY + (item & 1u)), ((item >> 1) & 1u) ^ 1u, wc) && lane == 0) {
             slot_of(item)->n = -1;
             mbar_arrive(bar(W_FULL + (item & 1u)));
         }

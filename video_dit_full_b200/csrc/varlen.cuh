@@ -19,14 +19,19 @@ __device__ __forceinline__ Span span_of(const int* cu, int n, int T) {
 // tile and each sequence starting a tile of its own: the sequence and the tile within it, or seq = -1
 // past the last.  The whole warp calls it; 32 sequences a step, so no table has to be built (and no
 // extra launch made) before the attention kernel.  Up to 32 sequences are taken longest first, so that
-// the work handed out last is short; more are taken as they come.
+// the work handed out last is short; more are taken as they come.  `from`
+// keeps the step where the last target was found: targets that grow are found from there on.
 struct TileAt {
     int seq, tile, tiles;          // tiles: of that sequence
 };
-__device__ __forceinline__ TileAt tile_at(const int* cu, int N, int T, int rows, int target) {
+struct ScanFrom {
+    int n0 = 0, before = 0;        // first sequence of the step, tiles before it
+};
+__device__ __forceinline__ TileAt tile_at(const int* cu, int N, int T, int rows, int target, ScanFrom& from) {
     const int lane = threadIdx.x & 31;
-    int before = 0;
-    for (int n0 = 0; n0 < N; n0 += 32) {
+    if (target < from.before) from = ScanFrom{};
+    int before = from.before;
+    for (int n0 = from.n0; n0 < N; n0 += 32) {
         const int mine = n0 + lane < N ? (span_of(cu, n0 + lane, T).len + rows - 1) / rows : 0;
         int upto;                                  // tiles up to and including this lane's sequence
         if (N <= 32) {
@@ -46,6 +51,8 @@ __device__ __forceinline__ TileAt tile_at(const int* cu, int N, int T, int rows,
         const unsigned here = __ballot_sync(0xffffffffu, before + upto > target && before + upto - mine <= target);
         if (here) {
             const int l = __ffs(here) - 1;
+            from.n0 = n0;
+            from.before = before;
             const int tiles = __shfl_sync(0xffffffffu, mine, l);
             return {n0 + l, target - before - __shfl_sync(0xffffffffu, upto, l) + tiles, tiles};
         }
