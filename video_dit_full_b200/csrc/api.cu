@@ -378,14 +378,14 @@ bool make_packed_map(CUtensorMap* m, const void* base, int T, int H, long long l
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tensor map over an fp32 accumulator [T, H, 128] as 3-D (128, H, T), box (`cols`, 1, 128); `swizzle`:
+// Tensor map over an fp32 accumulator [T, H, 128] as 3-D (128, H, T), box (`cols`, `heads`, 128 / `heads`); `swizzle`:
 // the 128-byte swizzle (cols = 32).
-bool make_packed_acc_map(CUtensorMap* m, void* base, int T, int H, int cols, bool swizzle) {
+bool make_packed_acc_map(CUtensorMap* m, void* base, int T, int H, int cols, int heads, bool swizzle) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[3] = {128, (cuuint64_t)H, (cuuint64_t)T};
     const cuuint64_t strides[2] = {128 * 4, (cuuint64_t)H * 128 * 4};
-    const cuuint32_t box[3] = {(cuuint32_t)cols, 1, 128};
+    const cuuint32_t box[3] = {(cuuint32_t)cols, (cuuint32_t)heads, (cuuint32_t)(128 / heads)};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -863,6 +863,8 @@ int wan_attn_varlen_bwd(const void* q, const void* k, const void* v, const void*
     p.splits = varlen_bwd_splits(N, Tq, Tk, H, Hkv);
     char* ws = static_cast<char*>(workspace);
     p.tile_bound = varlen_bwd_tile_bound(N, Tk);
+    const int pack = varlen_bwd_pack(H, Hkv);
+    while ((1 << p.pack_log2) < pack) ++p.pack_log2;
     const size_t off_delta = align256(size_t(Tq) * H * 128 * 4), off_order = off_delta + align256(size_t(Tq) * H * 4);
     const size_t off_end = off_order + align256(size_t(p.tile_bound) * 8), off_dk = off_end + align256(size_t(N) * 4);
     p.dq_acc = reinterpret_cast<float*>(ws);
@@ -874,13 +876,14 @@ int wan_attn_varlen_bwd(const void* q, const void* k, const void* v, const void*
         p.dv_acc = reinterpret_cast<float*>(ws + off_dk + align256(size_t(Tk) * Hkv * 128 * 4));
     }
     CUtensorMap tq{}, tk{}, tv{}, tdo{}, tdq{}, tdk{}, tdv{};        // those of an empty axis are never read
-    if (Tq > 0 && (!make_packed_map(&tq, q, Tq, H, ldq, 1, 128) || !make_packed_map(&tdo, dO, Tq, H, hd, 1, 128) ||
-                   !make_packed_acc_map(&tdq, p.dq_acc, Tq, H, 128, false)))
+    if (Tq > 0 && (!make_packed_map(&tq, q, Tq, H, ldq, pack, 128 / pack) ||
+                   !make_packed_map(&tdo, dO, Tq, H, hd, pack, 128 / pack) ||
+                   !make_packed_acc_map(&tdq, p.dq_acc, Tq, H, 128, pack, false)))
         return WAN_ATTN_ERR_CUDA;
     if (Tk > 0 && (!make_packed_map(&tk, k, Tk, Hkv, ldk, 1, 128) || !make_packed_map(&tv, v, Tk, Hkv, ldv, 1, 128)))
         return WAN_ATTN_ERR_CUDA;
-    if (p.splits > 1 && (!make_packed_acc_map(&tdk, p.dk_acc, Tk, Hkv, 32, true) ||
-                         !make_packed_acc_map(&tdv, p.dv_acc, Tk, Hkv, 32, true)))
+    if (p.splits > 1 && (!make_packed_acc_map(&tdk, p.dk_acc, Tk, Hkv, 32, 1, true) ||
+                         !make_packed_acc_map(&tdv, p.dv_acc, Tk, Hkv, 32, 1, true)))
         return WAN_ATTN_ERR_CUDA;
     return as_status(launch_varlen_bwd(tq, tk, tv, tdo, tdq, tdk, tdv, p, static_cast<cudaStream_t>(stream)));
 }

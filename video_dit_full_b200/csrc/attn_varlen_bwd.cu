@@ -9,8 +9,11 @@
 //   varlen_prep  D_i (fp32), zeroing of the fp32 dQ accumulator, and (one block) the key tiles of all
 //                sequences in the order of their work, most first
 //   varlen_main  one CTA per 128-key tile of a sequence and kv head.  K_j and V_j stay in shared memory
-//                while the CTA walks the 128-row Q tiles that see any of its keys, of every query head of
-//                the group in turn: dK and dV gather the group's sum in TMEM, with no atomics.  Per Q tile
+//                while the CTA walks the 128-row Q tiles that see any of its keys, of all query heads of the
+//                group: dK and dV gather the group's sum in TMEM, with no atomics.  A Q tile's rows are
+//                (token, query head) pairs, as many heads to a token as the largest power of two in the
+//                group: a short sequence then fills its tiles better (700 sequences of 1 to 30 tokens, 8
+//                heads over 2: 136 us against 254 with a head to a tile).  Per Q tile
 //                the five products of the dense backward, with the same roles (8 gradient warps, two
 //                threads per key row; TMA producer; tcgen05 issuer; dQ reducer):
 //                  S^T = K Q^T, dP^T = V dO^T;  dV += P^T dO;  dK += dS^T Q;  dQ^T = K^T dS^T -> TMA reduce-add
@@ -90,11 +93,29 @@ __device__ __forceinline__ void mma_ss_mn(uint32_t d, uint32_t a, uint32_t b, ui
 
 // The first Q tile that sees any key of key tile `tile` of a sequence, and how many do.
 __device__ __forceinline__ int first_q_tile(const VarlenBwdParams& p, Span sq, Span sk, int tile) {
-    return p.causal ? max(tile * BM - (sk.len - sq.len), 0) / BM : 0;
+    return p.causal ? max(tile * BM - (sk.len - sq.len), 0) / (BM >> p.pack_log2) : 0;
 }
 __device__ __forceinline__ int q_tiles(const VarlenBwdParams& p, Span sq, Span sk, int tile) {
-    return max((sq.len + BM - 1) / BM - first_q_tile(p, sq, sk, tile), 0);
+    const int tokens = BM >> p.pack_log2;
+    return max((sq.len + tokens - 1) / tokens - first_q_tile(p, sq, sk, tile), 0);
 }
+
+// A CTA's walk over its Q tiles: the tile, counted from the first, of the packed head, counted from the group's.
+struct Walk {
+    int tile, head, per_head;
+    __device__ __forceinline__ Walk(int it0, int per_head_) : tile(0), head(0), per_head(per_head_) {
+        if (per_head > 0) {
+            head = it0 / per_head;
+            tile = it0 - head * per_head;
+        }
+    }
+    __device__ __forceinline__ void next() {
+        if (++tile == per_head) {
+            tile = 0;
+            ++head;
+        }
+    }
+};
 
 // One warp: zero rows [first, 128) of a tile (two halves of d, a row 128 bytes of each).
 __device__ __forceinline__ void zero_rows(uint32_t tile, int first, int lane) {
@@ -121,9 +142,10 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     const Span sq = span_of(p.cu_q, at.x, p.Tq), sk = span_of(p.cu_k, at.x, p.Tk);
     const int kv0 = at.y * BM;
     const int shift = sk.len - sq.len;                    // causal: query i sees keys 0 .. i + shift
-    // Q tiles [i_first, i_first + per_head) of every head of the group; this split's run [it0, it0 + n)
+    // Q tiles [i_first, i_first + per_head) of every packed head; this split's run [it0, it0 + n)
+    const int pack_log2 = p.pack_log2, tokens = BM >> pack_log2;
     const int i_first = first_q_tile(p, sq, sk, at.y), per_head = q_tiles(p, sq, sk, at.y);
-    const int all = per_head * group;
+    const int all = per_head * (group >> pack_log2);
     const int it0 = static_cast<int>(static_cast<long long>(blockIdx.z) * all / p.splits);
     const int n = static_cast<int>(static_cast<long long>(blockIdx.z + 1) * all / p.splits) - it0;
 
@@ -200,11 +222,12 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             }
             const uint64_t keep = l2_policy_evict_last();
             int par[2] = {-1, -1};
-            for (int i = 0; i < n && ok; ++i) {
+            Walk at_tile(it0, per_head);
+            for (int i = 0; i < n && ok; ++i, at_tile.next()) {
                 const int s = i & 1;
                 const int use = (i >> 1) & 1;
-                const int it = it0 + i, h = hk * group + it / per_head, row0 = (i_first + it % per_head) * BM;
-                const int rows = min(sq.len - row0, BM);
+                const int h = hk * group + (at_tile.head << pack_log2), tok0 = (i_first + at_tile.tile) * tokens;
+                const int rows = min(sq.len - tok0, tokens) << pack_log2;
                 bool got = true;
                 if (lane == 0) got = wait_thread(bar(QDO_EMPTY + s), use ^ 1, wc);
                 ok = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
@@ -212,7 +235,7 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                 const uint32_t fb = bar(rows < BM ? EDGE : QDO_FULL + s);
                 if (lane == 0) {
                     mbar_arrive_expect_tx(fb, 2 * TILE_BYTES);
-                    const int tok = sq.begin + row0;
+                    const int tok = sq.begin + tok0;
                     tma_load_3d_hint(sQ(s), &tmq, fb, 0, h, tok, keep);
                     tma_load_3d_hint(sQ(s) + HALF_BYTES, &tmq, fb, 64, h, tok, keep);
                     tma_load_3d_hint(sDO(s), &tmdo, fb, 0, h, tok, keep);
@@ -301,12 +324,12 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         // ------------------ dQ reducer: TMA reduce-add of each dQ tile ------------
         if (lane == 0 && n > 0) {
             bool ok = true;
-            for (int i = 0; i < n && ok; ++i) {
+            Walk at_tile(it0, per_head);
+            for (int i = 0; i < n && ok; ++i, at_tile.next()) {
                 ok = wait_thread(bar(STAGED), i & 1, wc);
                 if (!ok) break;
-                const int it = it0 + i;
-                tma_reduce_add_3d(&tmdq, base + OFF_STAGE + (i & 1) * STAGE_BYTES, 0, hk * group + it / per_head,
-                                  sq.begin + (i_first + it % per_head) * BM);
+                tma_reduce_add_3d(&tmdq, base + OFF_STAGE + (i & 1) * STAGE_BYTES, 0, hk * group + (at_tile.head << pack_log2),
+                                  sq.begin + (i_first + at_tile.tile) * tokens);
                 bulk_commit_group();
                 bulk_wait_read_all();                         // the stage may be refilled now
                 mbar_arrive(bar(QDO_EMPTY + (i & 1)));
@@ -347,19 +370,24 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         // a tile's lse / D come from global memory one tile ahead, so their latency hides
         // behind the previous tile instead of delaying the wait for S^T
         float nl[2], nd[2];
-        auto load_vec = [&](int i) {
-            const int it = it0 + i;
-            const long long row = static_cast<long long>(hk * group + it / per_head) * p.Tq + sq.begin;
-            const int first = (i_first + it % per_head) * BM + cb;
+        Walk at_tile(it0, per_head), ahead = at_tile;
+        const int row0 = cb + lane, row1 = row0 + 32, heads = (1 << pack_log2) - 1;
+        const int tok_row[2] = {row0 >> pack_log2, row1 >> pack_log2};
+        const long long at_row[2] = {static_cast<long long>(row0 & heads) * p.Tq + tok_row[0],
+                                     static_cast<long long>(row1 & heads) * p.Tq + tok_row[1]};
+        auto load_vec = [&]() {
+            const int first = (i_first + ahead.tile) * tokens;
+            const long long at = static_cast<long long>(hk * group + (ahead.head << pack_log2)) * p.Tq + sq.begin + first;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int qi = first + e * 32 + lane;
-                nl[e] = qi < sq.len ? p.lse[row + qi] * LOG2E : 0.f;
-                nd[e] = qi < sq.len ? p.delta[row + qi] : 0.f;
+                const bool there = first + tok_row[e] < sq.len;
+                nl[e] = there ? p.lse[at + at_row[e]] * LOG2E : 0.f;
+                nd[e] = there ? p.delta[at + at_row[e]] : 0.f;
             }
+            ahead.next();
         };
-        if (n > 0) load_vec(0);
-        for (int i = 0; i < n && ok; ++i) {
+        if (n > 0) load_vec();
+        for (int i = 0; i < n && ok; ++i, at_tile.next()) {
             __syncwarp();                                    // previous tile's values no longer read
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -367,11 +395,12 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                 s_del[e * 32 + lane] = nd[e];
             }
             __syncwarp();
-            if (i + 1 < n) load_vec(i + 1);
-            // columns [lo, hi) of this half are queries of the sequence that see this key
-            const int first = (i_first + (it0 + i) % per_head) * BM + cb;
-            const int hi = key_ok ? sq.len - first : 0;
-            const int lo = p.causal ? key - shift - first : 0;
+            if (i + 1 < n) load_vec();
+            // columns [lo, hi) of this half are rows of the sequence that see this key
+            const int first = (i_first + at_tile.tile) * tokens;
+            const int rows = (min(sq.len - first, tokens) << pack_log2) - cb;       // rows of this half that exist
+            const int hi = key_ok ? rows : 0;
+            const int lo = p.causal ? (min(max(key - shift - first, 0), tokens) << pack_log2) - cb : 0;
             const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < 64);
 
             ok = wait_warp(bar(S_FULL), i & 1, wc);
@@ -447,7 +476,6 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             // fp32 [query][d] (its Q and dS^T are consumed), free the TMEM columns, and let the
             // reducer warp add the tile into the accumulator by TMA.
             float* stage = reinterpret_cast<float*>(smem + OFF_STAGE + (i & 1) * STAGE_BYTES);
-            const int rows = sq.len - first;                 // queries of this half that exist
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
                 uint32_t v[32];
@@ -661,6 +689,14 @@ int varlen_bwd_tile_bound(int N, int Tk) {
     return static_cast<int>(bound < Tk ? bound : Tk);
 }
 
+// Query heads that share a Q tile: the largest power of two that divides the group (and the tile's rows, so
+// that no row of a tile is left over).
+int varlen_bwd_pack(int H, int Hkv) {
+    const int group = H / Hkv;
+    int pack = group & -group;
+    return pack < varlen_bwd::BM ? pack : varlen_bwd::BM;
+}
+
 // CTAs among which a key tile's Q tiles are split: the number with the least estimated time, in units of
 // one Q tile's products (3.4 us measured).  Most work first, the CTAs finish together unless one is longer
 // than its SM's share: the larger of the two, with about 3 units of prologue and epilogue for every CTA;
@@ -670,7 +706,8 @@ int varlen_bwd_tile_bound(int N, int Tk) {
 // 0.32 ms split, 1.54 ms unsplit.
 int varlen_bwd_splits(int N, int Tq, int Tk, int H, int Hkv) {
     const double ctas = static_cast<double>(varlen_bwd_tile_bound(N, Tk)) * Hkv;
-    const double q_tiles = static_cast<double>((static_cast<long long>(Tq) / N + varlen_bwd::BM - 1) / varlen_bwd::BM) * (H / Hkv);
+    const int pack = varlen_bwd_pack(H, Hkv), tokens = varlen_bwd::BM / pack;
+    const double q_tiles = static_cast<double>((static_cast<long long>(Tq) / N + tokens - 1) / tokens) * (H / Hkv / pack);
     int best = 1;
     double least = 0;
     for (int s = 1; s <= 64 && s <= q_tiles; ++s) {

@@ -99,6 +99,7 @@ struct VarlenBwdParams : VarlenParams {
     float* dq_acc;                    // workspace fp32 [Tq, H, 128]: unscaled dS K
     float* delta;                     // workspace fp32 [H, Tq]: rowsum(dO * O)
     float *dk_acc, *dv_acc;           // workspace fp32 [Tk, Hkv, 128], splits > 1 only
+    int pack_log2;                    // log2 of the query heads that share a Q tile
     int tile_bound;                   // key tiles, an upper bound
     int2* order;                      // workspace [tile_bound]: key tiles as (sequence, tile), most work first
     int* tile_end;                    // workspace [N]: key tiles up to and including each sequence
@@ -158,13 +159,14 @@ int launch_varlen_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
                       const VarlenFwdParams& p, cudaStream_t stream);
 // How the forward lays out a call: heads per Q tile and splits of the keys (see VarlenFwdParams).
 void varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv, int* pack, int* splits);
-// tq, tk, tv, tdo: boxes (64, 1, 128); tdq: fp32 [Tq, H, 128], box (128, 1, 128); tdk, tdv: fp32
+// tk, tv: boxes (64, 1, 128); tq, tdo: (64, pack, 128 / pack); tdq: fp32 [Tq, H, 128], (128, pack, 128 / pack); tdk, tdv: fp32
 // [Tk, Hkv, 128], boxes (32, 1, 128) with the 128-byte swizzle, only read when p.splits > 1.
 int launch_varlen_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                       const CUtensorMap& tdq, const CUtensorMap& tdk, const CUtensorMap& tdv, const VarlenBwdParams& p,
                       cudaStream_t stream);
 int varlen_bwd_splits(int N, int Tq, int Tk, int H, int Hkv);
 int varlen_bwd_tile_bound(int N, int Tk);
+int varlen_bwd_pack(int H, int Hkv);
 
 // Int8 linear layer (int8_linear.cu) and its backward (int8_grad.cu).  0 on success.
 int launch_int8_quant_rows(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream);
