@@ -378,12 +378,16 @@ WAN_ATTN_API int wan_attn_bwd_noalloc(const void* q, const void* k, const void* 
  * were.  Inside a sequence q, k, v must be finite.  Offsets outside [0, T] or
  * decreasing are clipped, never followed.
  * Accumulation is fp32; P is rounded to bf16 for P V, as in wan_attn_fwd;
- * every exponential comes from the hardware exp2.
+ * every exponential comes from the hardware exp2.  Results do not depend on
+ * what else is in the batch, but for calls whose keys are split (below), where
+ * they may differ in their low bits with the split.  Deterministic.
  *   workspace, workspace_bytes : device memory, 256-byte aligned, of at least
  *             wan_attn_varlen_fwd_workspace_size bytes (0 for most sizes: the
  *             pointer may then be NULL).  Needed where few query rows face
- *             many keys: a sequence's keys are then split over several CTAs
- *             whose partial results are joined.
+ *             many keys: a sequence's keys are then split, and the parts'
+ *             normalised fp32 results and lse joined by a second kernel.
+ * The time that set_wait_budget_ns gives a wait holds within a work item; the
+ * kernel's scheduler, whose waits last as long as an item, has 64 times it.
  * Other conventions and errors as wan_attn_fwd.
  */
 WAN_ATTN_API size_t wan_attn_varlen_fwd_workspace_size(int N, int Tq, int Tk, int H, int Hkv, int D);
@@ -404,6 +408,8 @@ WAN_ATTN_API int wan_attn_varlen_fwd(const void* q, const void* k, const void* v
  * Rows of a sequence that no query sees get zero gradients; rows outside every
  * sequence are left as they were.  dQ (and dK, dV where few key tiles make the
  * call split them) is summed in fp32 in no fixed order, as in wan_attn_bwd.
+ * The workspace holds an fp32 dQ accumulator [Tq, H, D], D_i [H, Tq], the key
+ * tiles in the order of their work and, where split, fp32 dK and dV.
  */
 WAN_ATTN_API size_t wan_attn_varlen_bwd_workspace_size(int N, int Tq, int Tk, int H, int Hkv, int D);
 WAN_ATTN_API int wan_attn_varlen_bwd(const void* q, const void* k, const void* v, const void* o, const void* dO,

@@ -251,3 +251,51 @@ def test_captured_and_replayed(M):
     for a, b in zip(out, step()):
         assert torch.equal(a, b)
     wa.check_status()
+
+
+def test_stream_argument():
+    import torch
+    import video_dit_full_b200 as wa
+    _, _, wc, ws = weight(264, 1040, 3)
+    for M in (3, 300):
+        x, dy = bf16((M, 1040), 1).cuda(), bf16((M, 264), 2).cuda()
+        want = wa.int8_linear(x, wc, ws)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        y, codes, scales = wa.int8_linear(x, wc, ws, return_checkpoint=True, stream=s)
+        again = [wa.int8_linear(x, wc, ws, stream=s) for _ in range(5)]        # scratch reused in stream order
+        dw = wa.int8_grad_weight(dy, codes, scales, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        assert torch.equal(y, want) and all(torch.equal(a, want) for a in again)
+        assert torch.equal(dw, wa.int8_grad_weight(dy, codes, scales))
+    wa.check_status()
+
+
+def test_refused_tensors():
+    import torch
+    import video_dit_full_b200 as wa
+    x, dy = bf16((10, 64), 1).cuda(), bf16((10, 24), 2).cuda()
+    _, _, wc, ws = weight(24, 64, 3)
+    codes, scales = wa.int8_quantize_rows(x)
+    bad = [(lambda: wa.int8_linear(x.float(), wc, ws), TypeError), (lambda: wa.int8_linear(x[:, :48], wc, ws), ValueError),
+           (lambda: wa.int8_linear(x, wc, ws[:-1]), (TypeError, ValueError)), (lambda: wa.int8_linear(x.t(), wc, ws), ValueError),
+           (lambda: wa.int8_linear(x, wc.float(), ws), TypeError), (lambda: wa.int8_linear(x, wc, ws, bias=ws), TypeError),
+           (lambda: wa.int8_linear(x, wc[:20].contiguous(), ws[:20].contiguous()), wa.WanAttnError),       # N % 8
+           (lambda: wa.int8_quantize_rows(x[:, :40].contiguous()), wa.WanAttnError),                       # K % 16
+           (lambda: wa.int8_quantize_rows(x[0]), ValueError), (lambda: wa.int8_dequantize_rows(codes, scales[:-1]), (TypeError, ValueError)),
+           (lambda: wa.int8_grad_weight(dy[:-1], codes, scales), ValueError), (lambda: wa.int8_grad_input(dy, codes, scales), ValueError),
+           (lambda: wa.int8_grad_weight(dy, codes, scales, dw=dy), (TypeError, ValueError)),
+           (lambda: wa.int8_gemm(codes, scales, wc, ws, y=x), ValueError)]
+    for call, error in bad:
+        with pytest.raises(error):
+            call()
+
+
+def test_rows_without_a_finite_scale_show_in_the_gradients():
+    import torch
+    import video_dit_full_b200 as wa
+    x, dy = bf16((40, 64), 1), bf16((40, 24), 2).cuda()
+    x[7, 3] = float("inf")
+    codes, scales = wa.int8_quantize_rows(x.cuda())
+    assert torch.isnan(wa.int8_grad_weight(dy, codes, scales)).all()
+    wa.check_status()

@@ -34,7 +34,8 @@ FWD_ARGS = (*A[:7], 2, 300, 400, 4, 2, 128, 512, 256, 256, 1, A[7], 1 << 27, Non
     (dict(ldq=504), INVALID), (dict(ldk=260), INVALID), (dict(ldv=128), INVALID), (dict(q=at(A[0], 8)), INVALID),
     (dict(o=A[0]), INVALID), (dict(o=A[1]), INVALID), (dict(lse=A[3]), INVALID), (dict(lse=A[5]), INVALID),
     (dict(o=at(A[0], 512), ldq=1024), INVALID),
-    (dict(Tq=1 << 30, H=65536, Hkv=1, ldq=65536 * 128), INVALID)])
+    (dict(Tq=1 << 30, H=65536, Hkv=1, ldq=65536 * 128), INVALID), (dict(Tk=0x7fffffff), INVALID),
+    (dict(N=1 << 24, H=64, Hkv=2), INVALID)])
 def test_packed_forward(lib, kw, want):
     assert call(lib.wan_attn_varlen_fwd, FWD, FWD_ARGS, **kw) == want
 

@@ -270,3 +270,58 @@ def test_captured_and_replayed(case):
     for seed, (_, _, (o, lse, grads), *_) in zip((3, 4), graphs):
         x, cu_q, cu_k = make(lens_q, lens_k, H, Hkv, seed=seed)
         compare(x, cu_q, cu_k, causal, o, lse, grads)
+
+
+def test_stream_argument():
+    """A call given a stream runs, and allocates what it needs, there."""
+    import torch
+    import video_dit_full_b200 as wa
+    for case in ("grouped", "single_token_long"):
+        lens_q, lens_k, H, Hkv, causal = CASES[case]
+        x, cu_q, cu_k = make(lens_q, lens_k, H, Hkv, seed=11)
+        d, cq, ck = dev(x, cu_q, cu_k)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        o, lse, grads = run(d, cq, ck, causal, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        wa.check_status()
+        compare(x, cu_q, cu_k, causal, o, lse, grads)
+
+
+def test_the_rest_of_the_batch_does_not_matter():
+    """A sequence's forward is the same alone, in a batch, and at another place of it."""
+    import torch
+    import video_dit_full_b200 as wa
+    lens = [300, 77, 513]
+    x, cu, _ = make(lens, lens, 6, 2, seed=13)
+    d, c, _ = dev(x, cu, cu)
+    o, lse = wa.varlen_fwd(d["q"], d["k"], d["v"], c, c, causal=True)
+    for i, n in enumerate(lens):
+        part = [d[name][cu[i]:cu[i + 1]] for name in ("q", "k", "v")]
+        one = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        o1, lse1 = wa.varlen_fwd(*part, one, one, causal=True)
+        assert torch.equal(o1, o[cu[i]:cu[i + 1]]) and torch.equal(lse1, lse[:, cu[i]:cu[i + 1]])
+    wa.check_status()
+
+
+def test_refused_tensors():
+    import torch
+    import video_dit_full_b200 as wa
+    x, cu, _ = make([40, 9], [40, 9], 4, 2, seed=1)
+    d, c, _ = dev(x, cu, cu)
+    q, k, v = d["q"], d["k"], d["v"]
+    bad = [((q.float(), k, v, c, c), TypeError), ((q, k[:-1], v, c, c), ValueError), ((q, k, v, c.long(), c), TypeError),
+           ((q, k, v, c[:2], c), ValueError), ((q, k[:, :1].expand(-1, 3, -1), v[:, :1].expand(-1, 3, -1), c, c), ValueError),
+           ((q.transpose(0, 1), k, v, c, c), ValueError), ((q[..., :64], k[..., :64], v[..., :64], c, c), ValueError),
+           ((q[..., :64].contiguous(), k[..., :64].contiguous(), v[..., :64].contiguous(), c, c), wa.WanAttnError),
+           ((q, k, v, c[:1], c[:1]), ValueError)]
+    for args, error in bad:
+        with pytest.raises(error):
+            wa.varlen_fwd(*args)
+    o, lse = wa.varlen_fwd(q, k, v, c, c)
+    with pytest.raises(ValueError):
+        wa.varlen_bwd(q, k, v, o, d["do"], lse[:, :-1].contiguous(), c, c)
+    with pytest.raises(wa.WanAttnError):                    # a gradient over an input
+        wa.varlen_bwd(q, k, v, o, d["do"], lse, c, c, dq=q)
+    with pytest.raises(wa.WanAttnError):
+        wa.varlen_bwd(q, k, v, o, d["do"], lse, c, c, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))

@@ -419,7 +419,9 @@ bool packed_clash(const Packed& a, const Packed& b) {
 int check_packed(int N, int Tq, int Tk, int H, int Hkv, int D) {
     if (N < 1 || Tq < 0 || Tk < 0 || H < 1 || Hkv < 1 || D < 1 || H % Hkv) return WAN_ATTN_ERR_INVALID_ARG;
     if (D != 128) return WAN_ATTN_ERR_UNSUPPORTED;
-    if (H > 65535 || N > (1 << 24)) return WAN_ATTN_ERR_INVALID_ARG;
+    // token coordinates and grids stay in 32 bits
+    if (H > 65535 || Tq > 0x7fff0000 || Tk > 0x7fff0000 || N > (1 << 24) || double(N) * H >= double(1 << 30))
+        return WAN_ATTN_ERR_INVALID_ARG;
     const double lim = double(1ull << 40);
     if (double(Tq) * H * D >= lim || double(Tk) * Hkv * D >= lim) return WAN_ATTN_ERR_INVALID_ARG;
     return WAN_ATTN_OK;

@@ -354,9 +354,9 @@ def _need_torch():
     torch = module
 
 
-def _call_stream(stream, device):
-    """The stream's handle as an integer; the current stream of `device` if none is given."""
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+def _call_stream(device):
+    """The handle of the device's current stream as an integer."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _same_device(first, **others):
@@ -434,6 +434,9 @@ def varlen_fwd(q, k, v, cu_q, cu_k, causal=False, o=None, lse=None, workspace=No
     Rows of a given o / lse outside every sequence keep what they held; without one they are undefined."""
     if torch is None:
         _need_torch()
+    if stream is not None:             # what the call allocates then belongs to that stream too
+        with torch.cuda.stream(stream):
+            return varlen_fwd(q, k, v, cu_q, cu_k, causal, o, lse, workspace)
     N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv = _check_packed_call(q, k, v, cu_q, cu_k)
     if o is None:
         o = q.new_empty((Tq, H, D))
@@ -448,7 +451,7 @@ def varlen_fwd(q, k, v, cu_q, cu_k, causal=False, o=None, lse=None, workspace=No
     ws, ws_bytes, _keep = _workspace(so.wan_attn_varlen_fwd_workspace_size(N, Tq, Tk, H, Hkv, D), workspace, q)
     status = so.wan_attn_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
                                     cu_q.data_ptr(), cu_k.data_ptr(), N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv,
-                                    1 if causal else 0, ws, ws_bytes, _call_stream(stream, dev))
+                                    1 if causal else 0, ws, ws_bytes, _call_stream(dev))
     _check("wan_attn_varlen_fwd", status)
     return o, lse
 
@@ -462,6 +465,9 @@ def varlen_bwd(q, k, v, o, do, lse, cu_q, cu_k, causal=False, dq=None, dk=None, 
     """dQ, dK, dV of sum(O * dO) for packed sequences (``wan_attn_varlen_bwd``); given dq, dk, dv may be strided."""
     if torch is None:
         _need_torch()
+    if stream is not None:             # what the call allocates then belongs to that stream too
+        with torch.cuda.stream(stream):
+            return varlen_bwd(q, k, v, o, do, lse, cu_q, cu_k, causal, dq, dk, dv, workspace)
     N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv = _check_packed_call(q, k, v, cu_q, cu_k)
     _check_plain("o", o, torch.bfloat16, Tq * H * D)
     _check_plain("do", do, torch.bfloat16, Tq * H * D)
@@ -478,7 +484,7 @@ def varlen_bwd(q, k, v, o, do, lse, cu_q, cu_k, causal=False, dq=None, dk=None, 
     status = so.wan_attn_varlen_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
                                     lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_q.data_ptr(),
                                     cu_k.data_ptr(), N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv, lddq, lddk, lddv,
-                                    1 if causal else 0, ws, ws_bytes, _call_stream(stream, dev))
+                                    1 if causal else 0, ws, ws_bytes, _call_stream(dev))
     _check("wan_attn_varlen_bwd", status)
     return dq, dk, dv
 
@@ -515,6 +521,9 @@ def int8_quantize_rows(x, codes=None, scales=None, stream=None):
     an activation's 8-bit checkpoint, or a weight [N, K] with a scale per output channel."""
     if torch is None:
         _need_torch()
+    if stream is not None:             # what the call allocates then belongs to that stream too
+        with torch.cuda.stream(stream):
+            return int8_quantize_rows(x, codes, scales)
     M, K, ldx = _check_activations(x)
     codes = x.new_empty((M, K), dtype=torch.int8) if codes is None else codes
     scales = x.new_empty(M, dtype=torch.float32) if scales is None else scales
@@ -522,7 +531,7 @@ def int8_quantize_rows(x, codes=None, scales=None, stream=None):
     _check_plain("scales", scales, torch.float32, M)
     dev = _same_device(x, codes=codes, scales=scales)
     _check("wan_int8_quantize_rows", lib().wan_int8_quantize_rows(x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-                                                                  M, K, ldx, _call_stream(stream, dev)))
+                                                                  M, K, ldx, _call_stream(dev)))
     return codes, scales
 
 
@@ -530,13 +539,16 @@ def int8_dequantize_rows(codes, scales, x=None, stream=None):
     """bf16 [M, K] = codes * scales: an 8-bit checkpoint read back (``wan_int8_dequantize_rows``)."""
     if torch is None:
         _need_torch()
+    if stream is not None:             # what the call allocates then belongs to that stream too
+        with torch.cuda.stream(stream):
+            return int8_dequantize_rows(codes, scales, x)
     M, K = _check_matrix("codes", codes, torch.int8)
     _check_plain("scales", scales, torch.float32, M)
     x = codes.new_empty((M, K), dtype=torch.bfloat16) if x is None else x
     _check_plain("x", x, torch.bfloat16, M * K)
     dev = _same_device(codes, scales=scales, x=x)
     _check("wan_int8_dequantize_rows", lib().wan_int8_dequantize_rows(codes.data_ptr(), scales.data_ptr(),
-                                                                      x.data_ptr(), M, K, _call_stream(stream, dev)))
+                                                                      x.data_ptr(), M, K, _call_stream(dev)))
     return x
 
 
@@ -552,6 +564,9 @@ def int8_gemm(a_codes, a_scales, w_codes, w_scales, bias=None, y=None, stream=No
     """bf16 Y [M, N] = diag(a_scales) (a_codes w_codes^T) diag(w_scales) + bias through ``wan_int8_gemm``."""
     if torch is None:
         _need_torch()
+    if stream is not None:             # what the call allocates then belongs to that stream too
+        with torch.cuda.stream(stream):
+            return int8_gemm(a_codes, a_scales, w_codes, w_scales, bias, y)
     M, K = _check_matrix("a_codes", a_codes, torch.int8)
     _check_plain("a_scales", a_scales, torch.float32, M)
     N = _check_weight(w_codes, w_scales, bias, K)
@@ -560,7 +575,7 @@ def int8_gemm(a_codes, a_scales, w_codes, w_scales, bias=None, y=None, stream=No
     dev = _same_device(a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales, bias=bias, y=y)
     _check("wan_int8_gemm", lib().wan_int8_gemm(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(),
                                                 w_scales.data_ptr(), None if bias is None else bias.data_ptr(),
-                                                y.data_ptr(), M, N, K, _call_stream(stream, dev)))
+                                                y.data_ptr(), M, N, K, _call_stream(dev)))
     return y
 
 
@@ -570,6 +585,9 @@ def int8_linear(x, w_codes, w_scales, bias=None, return_checkpoint=False, stream
     codes of x that int8_grad_weight takes in the backward."""
     if torch is None:
         _need_torch()
+    if stream is not None:             # what the call allocates then belongs to that stream too
+        with torch.cuda.stream(stream):
+            return int8_linear(x, w_codes, w_scales, bias, return_checkpoint)
     M, K, ldx = _check_activations(x)
     N = _check_weight(w_codes, w_scales, bias, K)
     dev = _same_device(x, w_codes=w_codes, w_scales=w_scales, bias=bias)
@@ -583,7 +601,7 @@ def int8_linear(x, w_codes, w_scales, bias=None, return_checkpoint=False, stream
         scales_at = codes_at + M * K
     _check("wan_int8_linear", lib().wan_int8_linear(x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
                                                     None if bias is None else bias.data_ptr(), y.data_ptr(), codes_at,
-                                                    scales_at, M, N, K, ldx, _call_stream(stream, dev)))
+                                                    scales_at, M, N, K, ldx, _call_stream(dev)))
     return (y, codes, scales) if return_checkpoint else y
 
 
@@ -592,6 +610,9 @@ def int8_grad_weight(dy, codes, scales, dw=None, stream=None):
     (``wan_int8_grad_weight``)."""
     if torch is None:
         _need_torch()
+    if stream is not None:             # what the call allocates then belongs to that stream too
+        with torch.cuda.stream(stream):
+            return int8_grad_weight(dy, codes, scales, dw)
     M, N = _check_matrix("dy", dy, torch.bfloat16)
     rows, K = _check_matrix("codes", codes, torch.int8)
     if rows != M:
@@ -601,7 +622,7 @@ def int8_grad_weight(dy, codes, scales, dw=None, stream=None):
     _check_plain("dw", dw, torch.bfloat16, N * K)
     dev = _same_device(dy, codes=codes, scales=scales, dw=dw)
     _check("wan_int8_grad_weight", lib().wan_int8_grad_weight(dy.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-                                                              dw.data_ptr(), M, N, K, _call_stream(stream, dev)))
+                                                              dw.data_ptr(), M, N, K, _call_stream(dev)))
     return dw
 
 
@@ -610,6 +631,9 @@ def int8_grad_input(dy, w_codes, w_scales, dx=None, stream=None):
     (``wan_int8_grad_input``)."""
     if torch is None:
         _need_torch()
+    if stream is not None:             # what the call allocates then belongs to that stream too
+        with torch.cuda.stream(stream):
+            return int8_grad_input(dy, w_codes, w_scales, dx)
     M, N = _check_matrix("dy", dy, torch.bfloat16)
     rows, K = _check_matrix("w_codes", w_codes, torch.int8)
     if rows != N:
@@ -619,7 +643,7 @@ def int8_grad_input(dy, w_codes, w_scales, dx=None, stream=None):
     _check_plain("dx", dx, torch.bfloat16, M * K)
     dev = _same_device(dy, w_codes=w_codes, w_scales=w_scales, dx=dx)
     _check("wan_int8_grad_input", lib().wan_int8_grad_input(dy.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
-                                                            dx.data_ptr(), M, N, K, _call_stream(stream, dev)))
+                                                            dx.data_ptr(), M, N, K, _call_stream(dev)))
     return dx
 
 
