@@ -450,6 +450,10 @@ WAN_ATTN_API int wan_int8_gemm(const void* a_codes, const float* a_scales, const
  * The whole layer: quantises x into codes and scales, then multiplies.  codes
  * int8 [M, K] and scales fp32 [M] are outputs: kept, they are the layer's
  * 8-bit activation checkpoint (half of bf16's bytes) for the backward below.
+ * For a few tokens (up to 16, and as long as a slice of them fits an SM) the
+ * layer is one kernel, and codes and scales may be NULL if they are not
+ * wanted; where they are needed as scratch, NULL for both returns
+ * WAN_ATTN_ERR_WORKSPACE and enqueues nothing.
  */
 WAN_ATTN_API int wan_int8_linear(const void* x, const void* w_codes, const float* w_scales, const void* bias,
                                  void* y, void* codes, float* scales, int M, int N, int K, int64_t ldx,

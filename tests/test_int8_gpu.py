@@ -299,3 +299,28 @@ def test_rows_without_a_finite_scale_show_in_the_gradients():
     codes, scales = wa.int8_quantize_rows(x.cuda())
     assert torch.isnan(wa.int8_grad_weight(dy, codes, scales)).all()
     wa.check_status()
+
+
+@pytest.mark.parametrize("M,N,K,one_kernel", [(1, 5120, 5120, True), (16, 136, 2048, True), (5, 24, 8208, True), (5, 24, 20480, False),
+                                             (17, 136, 272, False)])
+def test_layer_without_a_checkpoint(M, N, K, one_kernel):
+    """Null codes and scales are taken where the layer is one kernel, and refused where they are its scratch."""
+    import torch
+    from video_dit_full_b200 import wan_attn
+    x = bf16((M, K), 3, outliers=True).cuda()
+    _, _, wc, ws = weight(N, K, 4)
+    want, codes, scales = wan_attn.int8_linear(x, wc, ws, return_checkpoint=True)
+    assert torch.equal(wan_attn.int8_linear(x, wc, ws), want)
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = wan_attn.lib().wan_int8_linear(x.data_ptr(), wc.data_ptr(), ws.data_ptr(), None, y.data_ptr(), None, None, M, N,
+                                            K, K, torch.cuda.current_stream().cuda_stream)
+    if one_kernel:
+        assert status == 0 and torch.equal(y, want)
+    else:
+        assert status == wan_attn.WORKSPACE and (y == 7).all()
+    only = torch.empty(M, device="cuda")
+    if one_kernel:
+        wan_attn.lib().wan_int8_linear(x.data_ptr(), wc.data_ptr(), ws.data_ptr(), None, y.data_ptr(), None, only.data_ptr(), M, N,
+                                       K, K, torch.cuda.current_stream().cuda_stream)
+        assert torch.equal(only, scales)
+    wan_attn.check_status()

@@ -503,9 +503,7 @@ int check_args(const Arg* a, int n) {
     return WAN_ATTN_OK;
 }
 
-// The int8 product on validated arguments.
-int int8_product(const void* a_codes, const float* a_scales, const void* b_codes, const float* b_scales,
-                 const void* bias, void* y, int M, int N, int K, bool after_quant, cudaStream_t stream) {
+Int8GemmParams int8_params(const float* a_scales, const float* b_scales, const void* bias, void* y, int M, int N, int K) {
     Int8GemmParams p;
     p.a_scales = a_scales;
     p.b_scales = b_scales;
@@ -514,9 +512,17 @@ int int8_product(const void* a_codes, const float* a_scales, const void* b_codes
     p.M = M;
     p.N = N;
     p.K = K;
-    p.after_quant = after_quant ? 1 : 0;
+    p.after_quant = 0;
     p.wait_budget_ns = wait_budget_ns();
     p.status = device_status_word();
+    return p;
+}
+
+// The int8 product on validated arguments.
+int int8_product(const void* a_codes, const float* a_scales, const void* b_codes, const float* b_scales,
+                 const void* bias, void* y, int M, int N, int K, bool after_quant, cudaStream_t stream) {
+    Int8GemmParams p = int8_params(a_scales, b_scales, bias, y, M, N, K);
+    p.after_quant = after_quant ? 1 : 0;
     if (!p.status) return WAN_ATTN_ERR_CUDA;
     const int tokens = int8_gemm_token_tile(M, N);
     CUtensorMap tx, tw;
@@ -933,9 +939,24 @@ int wan_int8_linear(const void* x, const void* w_codes, const float* w_scales, c
                      {w_scales, size_t(N) * 4, 3, false},           {y, size_t(M) * N * 2, 15, true},
                      {codes, size_t(M) * K, 15, true},              {scales, size_t(M) * 4, 3, true},
                      {bias, size_t(N) * 2, 15, false}};
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (int8_layer_fits(M, N, K)) {
+        // one launch; codes and scales are outputs only if they are given
+        Arg b[7] = {a[0], a[1], a[2], a[3]};
+        int n = 4;
+        if (codes) b[n++] = a[4];
+        if (scales) b[n++] = a[5];
+        if (bias) b[n++] = a[6];
+        const int sa = check_args(b, n);
+        if (sa != WAN_ATTN_OK) return sa;
+        const Int8GemmParams p = int8_params(nullptr, w_scales, bias, y, M, N, K);
+        CUtensorMap tw;
+        if (!p.status || !make_rows_u8_map(&tw, w_codes, N, K, 128)) return WAN_ATTN_ERR_CUDA;
+        return launch_int8_layer(tw, x, ldx, codes, scales, p, s) == 0 ? WAN_ATTN_OK : WAN_ATTN_ERR_CUDA;
+    }
+    if (!codes && !scales) return WAN_ATTN_ERR_WORKSPACE;
     const int sa = check_args(a, bias ? 7 : 6);
     if (sa != WAN_ATTN_OK) return sa;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (launch_int8_quant_rows(x, codes, scales, M, K, ldx, s) != 0) return WAN_ATTN_ERR_CUDA;
     return int8_product(codes, scales, w_codes, w_scales, bias, y, M, N, K, true, s);
 }

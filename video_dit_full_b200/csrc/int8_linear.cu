@@ -5,6 +5,7 @@
 //   gemm_pair      many tokens: CTA pairs (tcgen05 cta_group::2), 256 x 256 tiles, kind::i8 into int32 TMEM
 //   gemm_few       few tokens: the weight's 128 channels are the MMA's M, 16 to 128 tokens its N; a cluster
 //                  splits K and adds its exact int32 partial sums through distributed shared memory
+//   layer_few      the same with the quantiser inside: one launch for a layer of a few tokens
 // Sums are exact in int32 (K <= 131072), so neither the tiling nor the split changes a result.
 #include <cuda.h>
 
@@ -38,6 +39,26 @@ __device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, float pre, 
     const uint32_t c2 = code_of(b.x * pre, amax, inv), c3 = code_of(b.y * pre, amax, inv);
     return __byte_perm(__byte_perm(c0, c1, 0x0040), __byte_perm(c2, c3, 0x0040), 0x5410);
 }
+
+// What a row's absmax (as bf16 bits; an infinity or NaN is at least 0x7f80) makes of its values.
+struct RowScale {
+    float scale, pre, amax, inv;
+    bool bad;
+    __device__ __forceinline__ explicit RowScale(uint32_t amax_bits) {
+        const bool zero = amax_bits == 0;
+        bad = amax_bits >= 0x7f80u;
+        amax = __uint_as_float(amax_bits << 16);
+        scale = bad ? __uint_as_float(0x7fc00000u) : zero ? 1.f : __fdiv_rn(amax, 127.f);
+        // powers of two keep 127 x and 1 / amax inside fp32's range, and change no quotient
+        pre = bad || zero ? 0.f : amax < 0x1p-100f ? 0x1p100f : amax > 0x1p100f ? 0x1p-100f : 1.f;
+        amax = bad || zero ? 1.f : amax * pre;
+        inv = __frcp_rn(amax);
+    }
+    __device__ __forceinline__ uint2 codes8(uint4 u) const {
+        if (bad) u = make_uint4(0u, 0u, 0u, 0u);           // 0 * inf is not 0
+        return make_uint2(codes4(u.x, u.y, pre, amax, inv), codes4(u.z, u.w, pre, amax, inv));
+    }
+};
 
 // T threads per row (a power of two, 32 to 256), 256 / T rows per block.  Bound by memory: x is read once
 // (rows of up to 8 CACHED T elements stay in registers between the absmax and the codes), the codes written
@@ -76,22 +97,13 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16* __
 #pragma unroll
         for (int w = 0; w < T / 32; ++w) amax_bits = max(amax_bits, top[first + w]);
     }
-    const bool bad = amax_bits >= 0x7f80u, zero = amax_bits == 0;
-    float amax = __uint_as_float(amax_bits << 16);
-    if (here && tid == 0) scales[m] = bad ? __uint_as_float(0x7fc00000u) : zero ? 1.f : __fdiv_rn(amax, 127.f);
-    // powers of two keep 127 x and 1 / amax inside fp32's range, and change no quotient
-    const float pre = bad || zero ? 0.f : amax < 0x1p-100f ? 0x1p100f : amax > 0x1p100f ? 0x1p-100f : 1.f;
-    amax = bad || zero ? 1.f : amax * pre;
-    const float inv = __frcp_rn(amax);
+    const RowScale rs(amax_bits);
+    if (here && tid == 0) scales[m] = rs.scale;
     uint2* out = reinterpret_cast<uint2*>(codes + (here ? m : 0) * K);
-    auto put = [&](int c, uint4 u) {
-        if (bad) u = make_uint4(0u, 0u, 0u, 0u);           // 0 * inf is not 0
-        out[c] = make_uint2(codes4(u.x, u.y, pre, amax, inv), codes4(u.z, u.w, pre, amax, inv));
-    };
 #pragma unroll
     for (int c = 0; c < CACHED; ++c)
-        if (c * T + tid < pieces) put(c * T + tid, kept[c]);
-    for (int c = CACHED * T + tid; c < pieces; c += T) put(c, row[c]);
+        if (c * T + tid < pieces) out[c * T + tid] = rs.codes8(kept[c]);
+    for (int c = CACHED * T + tid; c < pieces; c += T) out[c] = rs.codes8(row[c]);
 }
 
 // T threads per row, 256 / T rows per block, 8 codes per thread and step (a warp's store is 512 bytes in one
@@ -379,6 +391,34 @@ struct Cfg {
     static_assert(2 * SMEM_BYTES <= 228 * 1024 - 2048, "two CTAs per SM");
 };
 
+// The cluster's partial tiles (at `base` in each CTA, [token][channel] int32) summed, scaled and stored: this
+// CTA takes tokens rank, rank + splits, ... of the tile, one warp a token, four channels a lane.
+template <int NT>
+__device__ __forceinline__ void store_tokens(const Int8GemmParams& p, uint32_t base, const float* sx, bool ok, int n0,
+                                             int m0, int rank, int splits, int warps) {
+    const int lane = lane_id(), n = n0 + lane * 4;
+    if (!ok || n >= p.N) return;
+    const float4 sw = make_float4(p.b_scales[n], p.b_scales[n + 1], p.b_scales[n + 2], p.b_scales[n + 3]);
+    float2 b01 = make_float2(0.f, 0.f), b23 = b01;
+    if (p.bias) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p.bias + n);
+        b01 = bf16x2_floats(u.x);
+        b23 = bf16x2_floats(u.y);
+    }
+    const int tokens = min(NT, p.M - m0);
+    for (int t = rank + (threadIdx.x >> 5) * splits; t < tokens; t += warps * splits) {
+        const uint32_t at = base + (t * 128 + lane * 4) * 4;
+        uint4 acc = make_uint4(0u, 0u, 0u, 0u);
+        for (int z = 0; z < splits; ++z) {
+            const uint4 v = ld_shared_cluster_v4(splits > 1 ? mapa_shared(at, z) : at);
+            acc = make_uint4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
+        }
+        *reinterpret_cast<uint2*>(p.y + static_cast<long long>(m0 + t) * p.N + n) =
+            make_uint2(pack_bf16x2(result(acc.x, sx[t], sw.x, b01.x), result(acc.y, sx[t], sw.y, b01.y)),
+                       pack_bf16x2(result(acc.z, sx[t], sw.z, b23.x), result(acc.w, sx[t], sw.w, b23.y)));
+    }
+}
+
 template <int NT>
 __global__ void __launch_bounds__(NTHREADS, 2)
 gemm_few_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_w,
@@ -451,7 +491,12 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant
             const uint32_t idesc = make_idesc(2, 1, 1, 0, 0, 128, NT);       // s32 <- s8 x s8, K-major
             for (int kb = 0; kb < nk; ++kb) {
                 const int s = kb % C::STAGES;
-                if (!wait_thread(bar(C::FULL + s), (kb / C::STAGES) & 1, wc)) break;
+                if (!wait_thread(bar(C::FULL + s), (kb / C::STAGES) & 1, wc)) {
+                    // what is in flight lands before the CTA's shared memory goes away
+                    for (int j = kb; j < min(nk, kb + C::STAGES); ++j)
+                        drain_wait(bar(C::FULL + j % C::STAGES), (j / C::STAGES) & 1);
+                    break;
+                }
                 tc_fence_after();
                 const uint32_t sa = base + s * C::STAGE_BYTES, sb = sa + C::A_BYTES;
 #pragma unroll
@@ -487,43 +532,275 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant
     if (splits > 1) cluster_sync_all();
     tc_fence_after();
 
-    // tokens rank, rank + splits, ... of the tile: one warp a token, four channels a lane
     if (p.after_quant) grid_dependency_wait();             // the scales are the quantiser's
-    const int n = n0 + lane * 4;
-    if (!*abort_flag && n < p.N) {
-        const float4 sw = make_float4(p.b_scales[n], p.b_scales[n + 1], p.b_scales[n + 2], p.b_scales[n + 3]);
-        float2 b01 = make_float2(0.f, 0.f), b23 = b01;
-        if (p.bias) {
-            const uint2 u = *reinterpret_cast<const uint2*>(p.bias + n);
-            b01 = bf16x2_floats(u.x);
-            b23 = bf16x2_floats(u.y);
-        }
-        const int tokens = min(NT, p.M - m0);
-        for (int t = rank + warp * splits; t < tokens; t += (NTHREADS / 32) * splits) {
-            const uint32_t at = base + (t * 128 + lane * 4) * 4;
-            uint4 acc = make_uint4(0u, 0u, 0u, 0u);
-            for (int z = 0; z < splits; ++z) {
-                const uint4 v = ld_shared_cluster_v4(splits > 1 ? mapa_shared(at, z) : at);
-                acc = make_uint4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
-            }
-            const float sx = p.a_scales[m0 + t];
-            *reinterpret_cast<uint2*>(p.y + static_cast<long long>(m0 + t) * p.N + n) =
-                make_uint2(pack_bf16x2(result(acc.x, sx, sw.x, b01.x), result(acc.y, sx, sw.y, b01.y)),
-                           pack_bf16x2(result(acc.z, sx, sw.z, b23.x), result(acc.w, sx, sw.w, b23.y)));
-        }
-    }
+    store_tokens<NT>(p, base, p.a_scales + m0, *abort_flag == 0, n0, m0, rank, splits, NTHREADS / 32);
     __syncthreads();
     if (splits > 1) cluster_sync_all();                    // no CTA leaves while a peer reads its partial tile
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
+// The layer for up to 16 tokens in one launch: bound by latency and by the weight's bytes.  While the weight's
+// first stages are on their way, each CTA of a cluster turns its own slice of K of the tokens into 8 bits,
+// straight into the swizzled operand, which stays for all of the CTA's stages.  A slice is read once and kept in
+// registers (LAYER_PIECES of 8 elements a thread); the row's absmax meets through distributed shared memory.
+// Every channel tile does so again; the few tokens come from L2.  The first tile's cluster also writes the
+// checkpoint, if one is asked for.  One token of 5120 -> 5120: 10 us for a call against 16 us with a quantiser
+// launched before it, most of both the host's; the two kernels overlap so well that in a graph they take
+// 8.2 us and this one 8.7, and with more tokens that gap grows (37 tokens of 1536 -> 8960: 8.2 and 11.4).
+constexpr int LAYER_TOKENS = 16, LAYER_PIECES = 8;         // pieces of the slice a thread keeps
+struct LayerCfg {
+    static constexpr int A_BYTES = 128 * BK, STAGES = 5;
+    static constexpr int X_BLOCK = LAYER_TOKENS * BK, X_MAX = 24 * 1024;     // a K block of codes; all of them
+    static constexpr int OFF_X = STAGES * A_BYTES;
+    static constexpr int OFF_ROW = OFF_X + X_MAX;                            // a token's pre, absmax, 1 / absmax, bad
+    static constexpr int OFF_TOP = OFF_ROW + LAYER_TOKENS * 16, OFF_SCALE = OFF_TOP + LAYER_TOKENS * 4;
+    static constexpr int OFF_BAR = OFF_SCALE + LAYER_TOKENS * 4;
+    static constexpr int FULL = 0, EMPTY = STAGES, READY = 2 * STAGES, DONE = 2 * STAGES + 1, NBARS = 2 * STAGES + 2;
+    static constexpr int OFF_TMEM_SLOT = OFF_BAR + NBARS * 8;
+    static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
+    static constexpr int SMEM_BYTES = OFF_ABORT + 8 + 1024;
+    static constexpr int NTHREADS = 320, QUANT = 256;                        // warp 0 TMA, 1 MMA, 2-9 quantiser
+    static constexpr uint32_t TMEM_COLS = 32;
+    static_assert(LAYER_TOKENS * 128 * 4 <= STAGES * A_BYTES, "the partial tile reuses the stages");
+    static_assert(2 * SMEM_BYTES <= 228 * 1024 - 2048, "two CTAs per SM");
+};
+
+struct LayerParams : Int8GemmParams {
+    const __nv_bfloat16* x;           // [M, K], ldx apart
+    long long ldx;
+    int8_t* codes;                    // [M, K] or null
+    float* scales;                    // [M] or null
+};
+
+__global__ void __launch_bounds__(LayerCfg::NTHREADS, 2)
+layer_few_kernel(const __grid_constant__ CUtensorMap tma_w, const LayerParams p) {
+    using C = LayerCfg;
+    constexpr int NT = LAYER_TOKENS;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;     // the same offset in every CTA
+    uint8_t* smem = smem_raw + (base - raw_addr);
+    const int warp = warp_id(), lane = lane_id();
+    const int splits = gridDim.x, rank = blockIdx.x;       // the cluster is the grid's x
+    const int n0 = blockIdx.y * 128;
+    const int nk_all = (p.K + BK - 1) / BK;
+    const int k0 = rank * nk_all / splits, nk = (rank + 1) * nk_all / splits - k0;
+    const uint32_t bar0 = base + C::OFF_BAR;
+    auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
+    const WaitCtl wc{abort_flag, p.wait_budget_ns, p.status};
+    uint32_t* top = reinterpret_cast<uint32_t*>(smem + C::OFF_TOP);
+    float* scale = reinterpret_cast<float*>(smem + C::OFF_SCALE);
+    float4* rows = reinterpret_cast<float4*>(smem + C::OFF_ROW);
+    const int pieces = (min(p.K, (k0 + nk) * BK) - k0 * BK) / 8;             // 8-element pieces of the slice
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(bar(C::FULL + s), 1);
+            mbar_init(bar(C::EMPTY + s), 1);
+        }
+        mbar_init(bar(C::READY), C::QUANT / 32);
+        mbar_init(bar(C::DONE), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        // the weight needs nothing of what follows
+        tma_prefetch_desc(&tma_w);
+        for (int kb = 0; kb < min(nk, C::STAGES); ++kb) {
+            mbar_arrive_expect_tx(bar(C::FULL + kb), C::A_BYTES);
+            tma_load_2d(base + kb * C::A_BYTES, &tma_w, bar(C::FULL + kb), (k0 + kb) * BK, n0);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc(base + C::OFF_TMEM_SLOT, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    // piece i * QUANT + q of the slice, token by token, is thread q's i-th
+    const int q = static_cast<int>(threadIdx.x) - 64;
+    auto piece_of = [&](int i, int per_token, int& t, int& c) {
+        const int at = i * C::QUANT + q;
+        t = at / per_token;
+        c = at - t * per_token;
+        return t < p.M;
+    };
+    auto load = [&](int t, int c) { return *reinterpret_cast<const uint4*>(p.x + t * p.ldx + c * 8); };
+    auto most_of = [](uint4 u) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t most = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        return most;
+    };
+    // the whole warp: into the token's absmax, with one atomic where its lanes hold one token
+    auto fold = [&](bool here, int t, uint32_t most) {
+        const int t0 = __shfl_sync(0xffffffffu, t, 0);
+        if (__all_sync(0xffffffffu, here && t == t0)) {
+            most = __reduce_max_sync(0xffffffffu, most);
+            if (lane == 0) atomicMax(top + t0, most);
+        } else if (here) {
+            atomicMax(top + t, most);
+        }
+    };
+    uint4 kept[LAYER_PIECES];
+    if (warp >= 2) {
+        if (q < NT) top[q] = 0;
+#pragma unroll
+        for (int i = 0; i < LAYER_PIECES; ++i) {
+            int t, c;
+            if (piece_of(i, pieces, t, c)) kept[i] = load(t, k0 * (BK / 8) + c);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp >= 2) {
+#pragma unroll
+        for (int i = 0; i < LAYER_PIECES; ++i) {
+            if (i * C::QUANT >= p.M * pieces) break;       // the same for every thread
+            int t, c;
+            const bool here = piece_of(i, pieces, t, c);
+            fold(here, t, here ? most_of(kept[i]) : 0u);
+        }
+    }
+    if (splits > 1) cluster_sync_all();        // the slices' absmax are there
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TMEM_SLOT);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            int issued = min(nk, C::STAGES);
+            for (int kb = issued; kb < nk; ++kb) {
+                const int s = kb % C::STAGES;
+                ok = wait_thread(bar(C::EMPTY + s), ((kb / C::STAGES) & 1) ^ 1, wc);
+                if (!ok) break;
+                mbar_arrive_expect_tx(bar(C::FULL + s), C::A_BYTES);
+                tma_load_2d(base + s * C::A_BYTES, &tma_w, bar(C::FULL + s), (k0 + kb) * BK, n0);
+                issued = kb + 1;
+            }
+            if (!ok)
+                for (int kb = max(0, issued - C::STAGES); kb < issued; ++kb)
+                    drain_wait(bar(C::FULL + kb % C::STAGES), (kb / C::STAGES) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = make_idesc(2, 1, 1, 0, 0, 128, NT);       // s32 <- s8 x s8, K-major
+            const bool ready = wait_thread(bar(C::READY), 0, wc);
+            for (int kb = 0; kb < nk; ++kb) {
+                const int s = kb % C::STAGES;
+                if (!ready || !wait_thread(bar(C::FULL + s), (kb / C::STAGES) & 1, wc)) {
+                    // what is in flight lands before the CTA's shared memory goes away
+                    for (int j = kb; j < min(nk, kb + C::STAGES); ++j)
+                        drain_wait(bar(C::FULL + j % C::STAGES), (j / C::STAGES) & 1);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sa = base + s * C::A_BYTES, sb = base + C::OFF_X + kb * C::X_BLOCK;
+#pragma unroll
+                for (int kk = 0; kk < BK / 32; ++kk)
+                    mma_i8_ss(tmem, sdesc_sw128(sa + kk * 32, 16, 1024), sdesc_sw128(sb + kk * 32, 16, 1024), idesc,
+                              (kb > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(bar(C::EMPTY + s));
+            }
+            mma_commit(bar(C::DONE));                      // all of this CTA's products, also after a time-out
+        }
+    } else {
+        named_bar_sync(1, C::QUANT);
+        if (q < p.M) {
+            uint32_t most = top[q];
+            for (int z = 0; z < splits; ++z)
+                if (z != rank) most = max(most, ld_shared_cluster_u32(mapa_shared(smem_u32(top + q), z)));
+            const RowScale rs(most);
+            scale[q] = rs.scale;
+            rows[q] = make_float4(rs.pre, rs.amax, rs.inv, rs.bad ? 1.f : 0.f);
+            if (p.scales && blockIdx.y == 0 && rank == 0) p.scales[q] = rs.scale;
+        }
+        named_bar_sync(1, C::QUANT);
+#pragma unroll
+        for (int i = 0; i < LAYER_PIECES; ++i) {
+            int t, c;
+            if (!piece_of(i, pieces, t, c)) break;
+            const float4 row = rows[t];
+            uint4 u = kept[i];
+            if (row.w != 0.f) u = make_uint4(0u, 0u, 0u, 0u);
+            const uint2 v = make_uint2(codes4(u.x, u.y, row.x, row.y, row.z), codes4(u.z, u.w, row.x, row.y, row.z));
+            // half of 16-byte chunk (c / 2) % 8 of row t of K block c / 16
+            const uint32_t at = sw128_chunk(base + C::OFF_X + (c >> 4) * C::X_BLOCK, t, (c >> 1) & 7) + (c & 1) * 8;
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(v.x), "r"(v.y) : "memory");
+            if (p.codes && blockIdx.y == 0)
+                *reinterpret_cast<uint2*>(p.codes + static_cast<long long>(t) * p.K + k0 * BK + c * 8) = v;
+        }
+        // rows behind the last token and codes behind K stay whatever they are: they meet other columns of the
+        // result, and zeros of the weight
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::READY));
+        if (warp < 6) {
+            // partial tile [token][channel] (int32) over the stages, which every MMA has read by now
+            if (wait_warp(bar(C::DONE), 0, wc)) {
+                tc_fence_after();
+                const int ch = (warp & 3) * 32 + lane;
+                const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+                int* part = reinterpret_cast<int*>(smem);
+#pragma unroll 1
+                for (int t = 0; t < NT; t += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(src + t, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) part[(t + e) * 128 + ch] = static_cast<int>(v[e]);
+                }
+            } else {
+                drain_wait(bar(C::DONE), 0);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (splits > 1) cluster_sync_all();
+    tc_fence_after();
+    store_tokens<NT>(p, base, scale, *abort_flag == 0, n0, 0, rank, splits, C::NTHREADS / 32);
+    __syncthreads();
+    if (splits > 1) cluster_sync_all();                    // no CTA leaves while a peer reads its partial tile
+    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// K is split while the CTAs stay within two per SM and each has two stages of K or more.
+int splits_for(int m_tiles, int N, int K) {
+    const int n_tiles = (N + 127) / 128, nk = (K + BK - 1) / BK;
+    int splits = 1;
+    while (splits < 8 && 2ll * splits * n_tiles * m_tiles <= 2 * 148 && nk / (2 * splits) >= 2) splits *= 2;
+    return splits;
+}
+
+// Whether a layer fits layer_few: the slices stay in registers, their codes in the operand that stays.
+bool layer_fits(int M, int N, int K) {
+    if (M > LAYER_TOKENS || N > 65535 * 128) return false;
+    const int nk = (K + BK - 1) / BK, splits = splits_for(1, N, K), most = (nk + splits - 1) / splits;
+    return most * LayerCfg::X_BLOCK <= LayerCfg::X_MAX && M * most * (BK / 8) <= LAYER_PIECES * LayerCfg::QUANT;
+}
+
+int launch_layer(const CUtensorMap& tw, const LayerParams& p, cudaStream_t stream) {
+    if (configure_smem(reinterpret_cast<const void*>(layer_few_kernel), LayerCfg::SMEM_BYTES) != 0) return -1;
+    const int splits = splits_for(1, p.N, p.K);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(splits, (p.N + 127) / 128);
+    cfg.blockDim = dim3(LayerCfg::NTHREADS);
+    cfg.dynamicSmemBytes = LayerCfg::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, layer_few_kernel, tw, p) == cudaSuccess ? 0 : -1;
+}
+
 template <int NT>
 int launch(const CUtensorMap& tx, const CUtensorMap& tw, const Int8GemmParams& p, cudaStream_t stream) {
     if (configure_smem(reinterpret_cast<const void*>(gemm_few_kernel<NT>), Cfg<NT>::SMEM_BYTES) != 0) return -1;
-    const int n_tiles = (p.N + 127) / 128, m_tiles = (p.M + NT - 1) / NT, nk = (p.K + BK - 1) / BK;
-    // K is split while the CTAs stay within two per SM and each has two stages of K or more
-    int splits = 1;
-    while (splits < 8 && 2ll * splits * n_tiles * m_tiles <= 2 * 148 && nk / (2 * splits) >= 2) splits *= 2;
+    const int n_tiles = (p.N + 127) / 128, m_tiles = (p.M + NT - 1) / NT;
+    const int splits = splits_for(m_tiles, p.N, p.K);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(splits, n_tiles, m_tiles);
     cfg.blockDim = dim3(NTHREADS);
@@ -573,6 +850,19 @@ int launch_int8_dequant_rows(const void* codes, const float* scales, void* x, in
     else if (K <= 8192) int8::launch_dequant<64>(codes, scales, x, M, K, stream);
     else int8::launch_dequant<256>(codes, scales, x, M, K, stream);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+bool int8_layer_fits(int M, int N, int K) { return int8::few::layer_fits(M, N, K); }
+
+int launch_int8_layer(const CUtensorMap& tw, const void* x, long long ldx, void* codes, float* scales,
+                      const Int8GemmParams& p, cudaStream_t stream) {
+    int8::few::LayerParams q;
+    static_cast<Int8GemmParams&>(q) = p;
+    q.x = static_cast<const __nv_bfloat16*>(x);
+    q.ldx = ldx;
+    q.codes = static_cast<int8_t*>(codes);
+    q.scales = scales;
+    return int8::few::launch_layer(tw, q, stream);
 }
 
 int int8_gemm_token_tile(int M, int N) {

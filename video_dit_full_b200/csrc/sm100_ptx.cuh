@@ -607,6 +607,11 @@ __device__ __forceinline__ uint4 ld_shared_cluster_v4(uint32_t addr) {
                  : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 // Programmatic dependent launch: let the stream's next kernel start (if it was launched to), and
 // wait until the kernel before this one has finished and its writes are visible.
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -171,6 +171,11 @@ int varlen_bwd_pack(int H, int Hkv);
 // Int8 linear layer (int8_linear.cu) and its backward (int8_grad.cu).  0 on success.
 int launch_int8_quant_rows(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream);
 int launch_int8_dequant_rows(const void* codes, const float* scales, void* x, int M, int K, cudaStream_t stream);
+// Whether a layer of this size runs in one launch (quantiser included; codes and scales may then be null),
+// and that launch.  tw: the weight's codes, boxes of 128 rows.
+bool int8_layer_fits(int M, int N, int K);
+int launch_int8_layer(const CUtensorMap& tw, const void* x, long long ldx, void* codes, float* scales,
+                      const Int8GemmParams& p, cudaStream_t stream);
 // Tokens of one tile of the few-token kernel for this size, or 0 for the CTA-pair kernel.
 int int8_gemm_token_tile(int M, int N);
 // tx: x's codes, boxes of the token tile's rows (128 for pairs); tw: the weight's codes, boxes of 128 rows.

@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(HERE, "libwan_attn.so")
 
 STATUS = {0: "WAN_ATTN_OK", 1: "WAN_ATTN_ERR_INVALID_ARG", 2: "WAN_ATTN_ERR_UNSUPPORTED",
           3: "WAN_ATTN_ERR_CUDA", 4: "WAN_ATTN_ERR_TIMEOUT", 5: "WAN_ATTN_ERR_WORKSPACE"}
+WORKSPACE = 5
 
 # (name, restype, argtypes) of every entry point the header declares
 _P, _I, _Z, _U64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64, ctypes.c_void_p
@@ -592,17 +593,21 @@ def int8_linear(x, w_codes, w_scales, bias=None, return_checkpoint=False, stream
     N = _check_weight(w_codes, w_scales, bias, K)
     dev = _same_device(x, w_codes=w_codes, w_scales=w_scales, bias=bias)
     y = x.new_empty((M, N))
+    call, bias_at = lib().wan_int8_linear, None if bias is None else bias.data_ptr()
     if return_checkpoint:
         codes, scales = x.new_empty((M, K), dtype=torch.int8), x.new_empty(M, dtype=torch.float32)
-        codes_at, scales_at = codes.data_ptr(), scales.data_ptr()
-    else:                                          # scratch: the codes, then the scales (K % 16 == 0)
-        scratch = x.new_empty(M * (K + 4), dtype=torch.uint8)
-        codes_at = scratch.data_ptr()
-        scales_at = codes_at + M * K
-    _check("wan_int8_linear", lib().wan_int8_linear(x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
-                                                    None if bias is None else bias.data_ptr(), y.data_ptr(), codes_at,
-                                                    scales_at, M, N, K, ldx, _call_stream(dev)))
-    return (y, codes, scales) if return_checkpoint else y
+        status = call(x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), bias_at, y.data_ptr(), codes.data_ptr(),
+                      scales.data_ptr(), M, N, K, ldx, _call_stream(dev))
+        _check("wan_int8_linear", status)
+        return y, codes, scales
+    status = WORKSPACE if M > 16 else call(x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), bias_at, y.data_ptr(),
+                                           None, None, M, N, K, ldx, _call_stream(dev))
+    if status == WORKSPACE:                        # too large to keep the codes on the SMs: scratch for the codes,
+        scratch = x.new_empty(M * (K + 4), dtype=torch.uint8)                   # then the scales (K % 16 == 0)
+        status = call(x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), bias_at, y.data_ptr(), scratch.data_ptr(),
+                      scratch.data_ptr() + M * K, M, N, K, ldx, _call_stream(dev))
+    _check("wan_int8_linear", status)
+    return y
 
 
 def int8_grad_weight(dy, codes, scales, dw=None, stream=None):
