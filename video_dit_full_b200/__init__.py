@@ -1,5 +1,8 @@
 """B200 (sm_100a) full spatio-temporal self-attention (and the text cross-attention) for Wan-style video DiTs.
 
+Beside them: packed attention (sequences of different lengths, causal, grouped heads), the FP8 and int8
+linear layers, and the int8 layer's backward from 8-bit activation checkpoints.
+
 The computation lives in ``libwan_attn.so`` (hand-written CUDA for sm_100a,
 C ABI in ``include/wan_attn.h``); ``wan_attn`` is its ctypes binding.
 """
