@@ -216,6 +216,27 @@ def test_bad_offsets_stay_in_bounds():
             assert (t[:200] == 7).all() and (t[200 + T:] == 7).all()
 
 
+def test_decreasing_offsets_of_many_sequences():
+    """Offsets that name 300,000 overlapping sequences of 8192 key tiles: their sum passes 2^31, the call's bounds hold."""
+    import torch
+    import video_dit_full_b200 as wa
+    T, N = 1 << 20, 600_001
+    k = torch.ones(T, 1, 128, dtype=torch.bfloat16, device="cuda")
+    q = torch.ones(4, 1, 128, dtype=torch.bfloat16, device="cuda")
+    cu_k = (torch.arange(N + 1, device="cuda") % 2 * T).to(torch.int32)
+    cu_q = torch.zeros(N + 1, dtype=torch.int32, device="cuda")
+    need = wa.varlen_bwd_workspace_size(N, 4, T, 1, 1)
+    ws = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+    grads = [torch.full((T + 256, 1, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    dq = torch.full_like(q, 7.0)
+    wa.varlen_bwd(q, k, k, q, q, torch.zeros(1, 4, device="cuda"), cu_q, cu_k, True, dq, grads[0][:T], grads[1][:T],
+                  workspace=ws[:need])
+    wa.check_status()
+    assert (ws[need:] == 77).all() and (dq == 7).all()
+    for g in grads:
+        assert (g[:128] == 0).all() and (g[T:] == 7).all()
+
+
 def test_many_sequences():
     import video_dit_full_b200 as wa
     rng = np.random.default_rng(0)

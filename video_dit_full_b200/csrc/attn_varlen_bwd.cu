@@ -567,17 +567,19 @@ __device__ void sort_tiles(const VarlenBwdParams& p) {
     for (int b = tid; b < BUCKETS; b += 256) count[b] = 0;
     if (tid == 0) carry = 0;
     __syncthreads();
-    // inclusive block scan of one value per thread, on top of what earlier steps summed to
+    // inclusive block scan of one value per thread, on top of what earlier steps summed to; sums stop at
+    // the bound (below 2^26), which offsets that are no offsets would pass, and 2^31 after it
     auto scan = [&](int v) {
+        v = min(v, p.tile_bound);
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, v, off);
-            if (lane >= off) v += o;
+            if (lane >= off) v = min(v + o, p.tile_bound);
         }
         if (lane == 31) sums[warp] = v;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) v += sums[w];
-        v += carry;
+        for (int w = 0; w < warp; ++w) v = min(v + sums[w], p.tile_bound);
+        v = min(v + carry, p.tile_bound);
         __syncthreads();
         if (tid == 255) carry = v;
         __syncthreads();
@@ -589,7 +591,7 @@ __device__ void sort_tiles(const VarlenBwdParams& p) {
         const int end = scan(n < p.N ? (span_of(p.cu_k, n, p.Tk).len + BM - 1) / BM : 0);
         if (n < p.N) p.tile_end[n] = end;
     }
-    const int total = min(carry, p.tile_bound);              // more only if the offsets are no offsets
+    const int total = carry;
     __syncthreads();
     auto place = [&](int x, int& seq, int& tile) {           // the first n with tile_end[n] > x
         int lo = 0, hi = p.N - 1;
