@@ -375,7 +375,8 @@ WAN_ATTN_API int wan_attn_bwd_noalloc(const void* q, const void* k, const void* 
  *   output need no copy).  Lengths of 0 are allowed.
  * A row that sees no key gets o = 0 and lse = -inf.  Rows outside every
  * sequence are not read into any result and their o and lse are left as they
- * were.  Inside a sequence q, k, v must be finite.  Offsets outside [0, T] or
+ * were.  Inside a sequence q, k, v must be finite; a row whose scores hold
+ * a NaN, or +inf, gets NaN.  Offsets outside [0, T] or
  * decreasing are clipped, never followed.
  * Accumulation is fp32; P is rounded to bf16 for P V, as in wan_attn_fwd;
  * every exponential comes from the hardware exp2.  Results do not depend on

@@ -237,6 +237,33 @@ def test_decreasing_offsets_of_many_sequences():
         assert (g[:128] == 0).all() and (g[T:] == 7).all()
 
 
+@pytest.mark.parametrize("lens_q,lens_k,H,Hkv", [([40, 300], [40, 300], 2, 2), ([1, 3], [700, 260], 8, 2),
+                                                 ([1], [20011], 8, 1), ([200, 5], [70, 0], 4, 4)])
+def test_nan_shows(lens_q, lens_k, H, Hkv):
+    """A NaN (or +inf) score shows in the rows that see it and in no other: a NaN query, a NaN key, scores of +inf."""
+    import torch
+    import video_dit_full_b200 as wa
+    x, cu_q, cu_k = make(lens_q, lens_k, H, Hkv, seed=8)
+    d, cq, ck = dev(x, cu_q, cu_k)
+    want, _ = wa.varlen_fwd(d["q"], d["k"], d["v"], cq, ck, causal=True)
+    q = d["q"].clone()
+    row = lens_q[0] - 1                                         # its last row sees every key
+    q[row, H - 1] = float("nan")
+    o, lse = wa.varlen_fwd(q, d["k"], d["v"], cq, ck, causal=True)
+    assert o[row, H - 1].isnan().all() and lse[H - 1, row].isnan()
+    o[row, H - 1] = want[row, H - 1]
+    assert torch.equal(o, want)
+    for bad in (float("nan"), 3e38):                            # 3e38 times a positive query: +inf
+        k, q = d["k"].clone(), d["q"].abs()
+        plain, _ = wa.varlen_fwd(q, k, d["v"], cq, ck, causal=True)
+        k[lens_k[0] - 1] = bad                                  # the last key: only the last row of sequence 0 sees it
+        o, lse = wa.varlen_fwd(q, k, d["v"], cq, ck, causal=True)
+        assert o[row].isnan().all() and lse[:, row].isnan().all()
+        o[row] = plain[row]
+        assert torch.equal(o, plain)
+    wa.check_status()
+
+
 def test_many_sequences():
     import video_dit_full_b200 as wa
     rng = np.random.default_rng(0)

@@ -551,7 +551,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
             const int row_tok = r / p.pack, i_tile = WORK(w, i0) + (shared ? 0 : t * tile_tokens), q_len = WORK(w, q_len);
             const int head = WORK(w, h0) + r - row_tok * p.pack, token = WORK(w, q_begin) + i_tile + row_tok;
             const bool real = row_tok < tile_tokens && i_tile + row_tok < q_len && !(shared && t == 1);
-            const bool empty = m_ref == -INFINITY;            // the row saw no key here
+            const bool empty = l == 0.f;                      // the row saw no key here (a NaN score leaves l NaN: it shows)
             const bool by_tma = p.splits == 1 && i_tile + tile_tokens <= q_len && nt > 0 && !shared;
             const uint32_t stage = sQ + t * TILE_BYTES;
             if (ok && !(shared && t == 1)) {
@@ -661,12 +661,12 @@ __global__ void __launch_bounds__(128) varlen_join_kernel(const VarlenFwdParams 
         l += w;
         acc = make_float4(fmaf(w, o.x, acc.x), fmaf(w, o.y, acc.y), fmaf(w, o.z, acc.z), fmaf(w, o.w, acc.w));
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;       // a NaN shows
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * HD + lane * 4) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (lane == 0)
         p.lse[static_cast<long long>(head) * p.Tq + token] =
-            l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 // CTAs along the tile axis, an upper bound from the sizes alone: every sequence wastes less than one tile.
