@@ -1,4 +1,5 @@
-"""Thin ctypes binding of ``libwan_attn.so`` (the C ABI in ``include/wan_attn.h``).
+"""Thin binding of ``libwan_attn.so`` (the C ABI in ``include/wan_attn.h``): ctypes, and for the packed
+attention and int8 calls the extension module ``_bind`` (``csrc/bind.cpp``).
 
 Argument marshalling only: torch tensors are checked for dtype, device, shape
 and contiguity, and their device pointers and the current CUDA stream are
@@ -13,6 +14,7 @@ import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libwan_attn.so")
+BIND_PATH = os.path.join(HERE, "_bind.so")
 
 STATUS = {0: "WAN_ATTN_OK", 1: "WAN_ATTN_ERR_INVALID_ARG", 2: "WAN_ATTN_ERR_UNSUPPORTED",
           3: "WAN_ATTN_ERR_CUDA", 4: "WAN_ATTN_ERR_TIMEOUT", 5: "WAN_ATTN_ERR_WORKSPACE"}
@@ -346,82 +348,45 @@ def fp8_linear(x, w_codes, w_scale, stream=None):
     return fp8_gemm(codes, scales, w_codes, w_scale, stream=stream)
 
 
-torch = None                       # the module, once a call below has needed it
+# Entry points that the binding in csrc/bind.cpp calls, in its order.
+_BOUND = ("wan_attn_varlen_fwd_workspace_size", "wan_attn_varlen_fwd", "wan_attn_varlen_bwd_workspace_size",
+          "wan_attn_varlen_bwd", "wan_int8_quantize_rows", "wan_int8_dequantize_rows", "wan_int8_gemm", "wan_int8_linear",
+          "wan_int8_grad_weight", "wan_int8_grad_input")
+_bound = None
 
 
-def _need_torch():
-    global torch
-    import torch as module
-    torch = module
+def _binding():
+    """The extension module ``_bind`` on the loaded library: the packed attention and int8 calls' checks of
+    their tensors, their outputs and the call, in C++ (raises if it has not been built)."""
+    global _bound
+    if _bound is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (the module is linked against it)
+        if not os.path.exists(BIND_PATH):
+            raise RuntimeError(f"{BIND_PATH} is missing: run `python -m video_dit_full_b200.build`")
+        spec = importlib.util.spec_from_loader("_bind", importlib.machinery.ExtensionFileLoader("_bind", BIND_PATH))
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        so = lib()
+        module.bind(*[ctypes.cast(getattr(so, name), ctypes.c_void_p).value for name in _BOUND])
+        _bound = module
+    return _bound
 
 
-def _call_stream(device):
-    """The handle of the device's current stream as an integer."""
-    return torch._C._cuda_getCurrentRawStream(device)
+def _bound_call(call, name, *args):
+    """A call through the binding: its outputs, or WanAttnError for the status that it returns instead."""
+    out = getattr(_bound or _binding(), call)(*args)
+    if type(out) is int:
+        raise WanAttnError(name, out)
+    return out
 
 
-def _same_device(first, **others):
-    """The index of the one device that every tensor is on, which must be the current one (the device
-    whose context and stream the call uses)."""
-    dev = torch.cuda.current_device()
-    if first.get_device() != dev:
-        raise ValueError(f"the tensors are on {first.device}, the current device is cuda:{dev}")
-    for name, t in others.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    return dev
-
-
-def _check_packed(name, t, shape=None):
-    """A bf16 [T, H, D] CUDA tensor whose tokens may be strided; returns the token stride in elements."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, D]")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    T, H, D = t.shape
-    row = H * D
-    if t.is_contiguous():
-        return row
-    ld, sh, sd = t.stride()
-    if T == 1:
-        ld = row                                   # one token: its stride means nothing
-    if (D > 1 and sd != 1) or (H > 1 and sh != D) or ld < row or ld % 8:
-        raise ValueError(f"{name} must hold each token's [H, D] contiguously, tokens a multiple of 8 elements apart")
-    return ld
-
-
-def _check_offsets(name, t):
-    _check_plain(name, t, torch.int32)
-    if t.dim() != 1 or t.shape[0] < 2:
-        raise ValueError(f"{name} must be [sequences + 1]")
-
-
-def _check_packed_call(q, k, v, cu_q, cu_k):
-    ldq, ldk = _check_packed("q", q), _check_packed("k", k)
-    ldv = _check_packed("v", v, k.shape)
-    Tq, H, D = q.shape
-    Tk, Hkv, Dk = k.shape
-    if Dk != D or Hkv < 1 or H % Hkv:
-        raise ValueError(f"k has shape {tuple(k.shape)}: its heads must divide q's {H}, its D be {D}")
-    _check_offsets("cu_q", cu_q)
-    if cu_k is not cu_q:
-        _check_offsets("cu_k", cu_k)
-        if cu_q.shape != cu_k.shape:
-            raise ValueError("cu_q and cu_k must name the same number of sequences")
-    return cu_q.shape[0] - 1, Tq, Tk, H, Hkv, D, ldq, ldk, ldv
-
-
-def _workspace(need, given, like):
-    """(pointer, bytes, tensor to keep) of the given workspace, or of a new one if the call needs any."""
-    if given is None:
-        if not need:
-            return None, 0, None
-        given = like.new_empty(need, dtype=torch.uint8)
-    return given.data_ptr(), given.numel() * given.element_size(), given
+def _on(stream):
+    """What a call given a stream runs under: what it allocates then belongs to that stream too."""
+    import torch
+    return torch.cuda.stream(stream)
 
 
 def varlen_fwd_workspace_size(N, Tq, Tk, H, Hkv, D=128) -> int:
@@ -433,28 +398,10 @@ def varlen_fwd(q, k, v, cu_q, cu_k, causal=False, o=None, lse=None, workspace=No
     may be strided), sequence n at rows cu_q[n]:cu_q[n+1] and cu_k[n]:cu_k[n+1] (int32, on the device).
 
     Rows of a given o / lse outside every sequence keep what they held; without one they are undefined."""
-    if torch is None:
-        _need_torch()
-    if stream is not None:             # what the call allocates then belongs to that stream too
-        with torch.cuda.stream(stream):
+    if stream is not None:
+        with _on(stream):
             return varlen_fwd(q, k, v, cu_q, cu_k, causal, o, lse, workspace)
-    N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv = _check_packed_call(q, k, v, cu_q, cu_k)
-    if o is None:
-        o = q.new_empty((Tq, H, D))
-    else:
-        _check_plain("o", o, torch.bfloat16, Tq * H * D)
-    if lse is None:
-        lse = q.new_empty((H, Tq), dtype=torch.float32)
-    else:
-        _check_plain("lse", lse, torch.float32, H * Tq)
-    dev = _same_device(q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, o=o, lse=lse, workspace=workspace)
-    so = lib()
-    ws, ws_bytes, _keep = _workspace(so.wan_attn_varlen_fwd_workspace_size(N, Tq, Tk, H, Hkv, D), workspace, q)
-    status = so.wan_attn_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                    cu_q.data_ptr(), cu_k.data_ptr(), N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv,
-                                    1 if causal else 0, ws, ws_bytes, _call_stream(dev))
-    _check("wan_attn_varlen_fwd", status)
-    return o, lse
+    return _bound_call("varlen_fwd", "wan_attn_varlen_fwd", q, k, v, cu_q, cu_k, causal, o, lse, workspace)
 
 
 def varlen_bwd_workspace_size(N, Tq, Tk, H, Hkv, D=128) -> int:
@@ -464,192 +411,64 @@ def varlen_bwd_workspace_size(N, Tq, Tk, H, Hkv, D=128) -> int:
 def varlen_bwd(q, k, v, o, do, lse, cu_q, cu_k, causal=False, dq=None, dk=None, dv=None, workspace=None,
                stream=None):
     """dQ, dK, dV of sum(O * dO) for packed sequences (``wan_attn_varlen_bwd``); given dq, dk, dv may be strided."""
-    if torch is None:
-        _need_torch()
-    if stream is not None:             # what the call allocates then belongs to that stream too
-        with torch.cuda.stream(stream):
+    if stream is not None:
+        with _on(stream):
             return varlen_bwd(q, k, v, o, do, lse, cu_q, cu_k, causal, dq, dk, dv, workspace)
-    N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv = _check_packed_call(q, k, v, cu_q, cu_k)
-    _check_plain("o", o, torch.bfloat16, Tq * H * D)
-    _check_plain("do", do, torch.bfloat16, Tq * H * D)
-    _check_plain("lse", lse, torch.float32, H * Tq)
-    dq = q.new_empty((Tq, H, D)) if dq is None else dq
-    dk = q.new_empty((Tk, Hkv, D)) if dk is None else dk
-    dv = q.new_empty((Tk, Hkv, D)) if dv is None else dv
-    lddq = _check_packed("dq", dq, q.shape)
-    lddk, lddv = _check_packed("dk", dk, k.shape), _check_packed("dv", dv, k.shape)
-    dev = _same_device(q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, o=o, do=do, lse=lse, dq=dq, dk=dk, dv=dv,
-                       workspace=workspace)
-    so = lib()
-    ws, ws_bytes, _keep = _workspace(so.wan_attn_varlen_bwd_workspace_size(N, Tq, Tk, H, Hkv, D), workspace, q)
-    status = so.wan_attn_varlen_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
-                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_q.data_ptr(),
-                                    cu_k.data_ptr(), N, Tq, Tk, H, Hkv, D, ldq, ldk, ldv, lddq, lddk, lddv,
-                                    1 if causal else 0, ws, ws_bytes, _call_stream(dev))
-    _check("wan_attn_varlen_bwd", status)
-    return dq, dk, dv
-
-
-def _check_matrix(name, t, dtype, cols=None):
-    """A contiguous 2-D CUDA tensor; returns its shape."""
-    _check_plain(name, t, dtype)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    if cols is not None and t.shape[1] != cols:
-        raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
-    return t.shape
-
-
-def _check_activations(x):
-    """bf16 [M, K] whose rows may be strided; returns M, K and the row stride in elements."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.bfloat16:
-        raise TypeError("x must be a bfloat16 CUDA tensor")
-    if x.dim() != 2:
-        raise ValueError("x must be [M, K]")
-    M, K = x.shape
-    if x.is_contiguous():
-        return M, K, K
-    ld, sk = x.stride()
-    if M == 1:
-        ld = K                                     # one row: its stride means nothing
-    if (K > 1 and sk != 1) or ld < K or ld % 8:
-        raise ValueError("x must hold each row contiguously, rows a multiple of 8 elements apart")
-    return M, K, ld
+    return _bound_call("varlen_bwd", "wan_attn_varlen_bwd", q, k, v, cu_q, cu_k, causal, o, do, lse, dq, dk, dv,
+                       workspace)
 
 
 def int8_quantize_rows(x, codes=None, scales=None, stream=None):
     """int8 codes [M, K] and fp32 scales [M] of bf16 x [M, K], a scale per row (``wan_int8_quantize_rows``):
     an activation's 8-bit checkpoint, or a weight [N, K] with a scale per output channel."""
-    if torch is None:
-        _need_torch()
-    if stream is not None:             # what the call allocates then belongs to that stream too
-        with torch.cuda.stream(stream):
+    if stream is not None:
+        with _on(stream):
             return int8_quantize_rows(x, codes, scales)
-    M, K, ldx = _check_activations(x)
-    codes = x.new_empty((M, K), dtype=torch.int8) if codes is None else codes
-    scales = x.new_empty(M, dtype=torch.float32) if scales is None else scales
-    _check_plain("codes", codes, torch.int8, M * K)
-    _check_plain("scales", scales, torch.float32, M)
-    dev = _same_device(x, codes=codes, scales=scales)
-    _check("wan_int8_quantize_rows", lib().wan_int8_quantize_rows(x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-                                                                  M, K, ldx, _call_stream(dev)))
-    return codes, scales
+    return _bound_call("int8_quantize_rows", "wan_int8_quantize_rows", x, codes, scales)
 
 
 def int8_dequantize_rows(codes, scales, x=None, stream=None):
     """bf16 [M, K] = codes * scales: an 8-bit checkpoint read back (``wan_int8_dequantize_rows``)."""
-    if torch is None:
-        _need_torch()
-    if stream is not None:             # what the call allocates then belongs to that stream too
-        with torch.cuda.stream(stream):
+    if stream is not None:
+        with _on(stream):
             return int8_dequantize_rows(codes, scales, x)
-    M, K = _check_matrix("codes", codes, torch.int8)
-    _check_plain("scales", scales, torch.float32, M)
-    x = codes.new_empty((M, K), dtype=torch.bfloat16) if x is None else x
-    _check_plain("x", x, torch.bfloat16, M * K)
-    dev = _same_device(codes, scales=scales, x=x)
-    _check("wan_int8_dequantize_rows", lib().wan_int8_dequantize_rows(codes.data_ptr(), scales.data_ptr(),
-                                                                      x.data_ptr(), M, K, _call_stream(dev)))
-    return x
-
-
-def _check_weight(w_codes, w_scales, bias, K):
-    N, _ = _check_matrix("w_codes", w_codes, torch.int8, K)
-    _check_plain("w_scales", w_scales, torch.float32, N)
-    if bias is not None:
-        _check_plain("bias", bias, torch.bfloat16, N)
-    return N
+    return _bound_call("int8_dequantize_rows", "wan_int8_dequantize_rows", codes, scales, x)
 
 
 def int8_gemm(a_codes, a_scales, w_codes, w_scales, bias=None, y=None, stream=None):
     """bf16 Y [M, N] = diag(a_scales) (a_codes w_codes^T) diag(w_scales) + bias through ``wan_int8_gemm``."""
-    if torch is None:
-        _need_torch()
-    if stream is not None:             # what the call allocates then belongs to that stream too
-        with torch.cuda.stream(stream):
+    if stream is not None:
+        with _on(stream):
             return int8_gemm(a_codes, a_scales, w_codes, w_scales, bias, y)
-    M, K = _check_matrix("a_codes", a_codes, torch.int8)
-    _check_plain("a_scales", a_scales, torch.float32, M)
-    N = _check_weight(w_codes, w_scales, bias, K)
-    y = a_codes.new_empty((M, N), dtype=torch.bfloat16) if y is None else y
-    _check_plain("y", y, torch.bfloat16, M * N)
-    dev = _same_device(a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales, bias=bias, y=y)
-    _check("wan_int8_gemm", lib().wan_int8_gemm(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(),
-                                                w_scales.data_ptr(), None if bias is None else bias.data_ptr(),
-                                                y.data_ptr(), M, N, K, _call_stream(dev)))
-    return y
+    return _bound_call("int8_gemm", "wan_int8_gemm", a_codes, a_scales, w_codes, w_scales, bias, y)
 
 
 def int8_linear(x, w_codes, w_scales, bias=None, return_checkpoint=False, stream=None):
     """Y = the int8 linear layer of bf16 x [M, K] (rows may be strided) with a weight quantised by
     int8_quantize_rows (``wan_int8_linear``).  With return_checkpoint: (Y, codes, scales), the 8-bit
     codes of x that int8_grad_weight takes in the backward."""
-    if torch is None:
-        _need_torch()
-    if stream is not None:             # what the call allocates then belongs to that stream too
-        with torch.cuda.stream(stream):
+    if stream is not None:
+        with _on(stream):
             return int8_linear(x, w_codes, w_scales, bias, return_checkpoint)
-    M, K, ldx = _check_activations(x)
-    N = _check_weight(w_codes, w_scales, bias, K)
-    dev = _same_device(x, w_codes=w_codes, w_scales=w_scales, bias=bias)
-    y = x.new_empty((M, N))
-    call, bias_at = lib().wan_int8_linear, None if bias is None else bias.data_ptr()
-    if return_checkpoint:
-        codes, scales = x.new_empty((M, K), dtype=torch.int8), x.new_empty(M, dtype=torch.float32)
-        status = call(x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), bias_at, y.data_ptr(), codes.data_ptr(),
-                      scales.data_ptr(), M, N, K, ldx, _call_stream(dev))
-        _check("wan_int8_linear", status)
-        return y, codes, scales
-    status = WORKSPACE if M > 16 else call(x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), bias_at, y.data_ptr(),
-                                           None, None, M, N, K, ldx, _call_stream(dev))
-    if status == WORKSPACE:                        # too large to keep the codes on the SMs: scratch for the codes,
-        scratch = x.new_empty(M * (K + 4), dtype=torch.uint8)                   # then the scales (K % 16 == 0)
-        status = call(x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), bias_at, y.data_ptr(), scratch.data_ptr(),
-                      scratch.data_ptr() + M * K, M, N, K, ldx, _call_stream(dev))
-    _check("wan_int8_linear", status)
-    return y
+    return _bound_call("int8_linear", "wan_int8_linear", x, w_codes, w_scales, bias, return_checkpoint)
 
 
 def int8_grad_weight(dy, codes, scales, dw=None, stream=None):
     """bf16 dW [N, K] = dY^T (codes * scales) from dY [M, N] and the layer input's 8-bit checkpoint
     (``wan_int8_grad_weight``)."""
-    if torch is None:
-        _need_torch()
-    if stream is not None:             # what the call allocates then belongs to that stream too
-        with torch.cuda.stream(stream):
+    if stream is not None:
+        with _on(stream):
             return int8_grad_weight(dy, codes, scales, dw)
-    M, N = _check_matrix("dy", dy, torch.bfloat16)
-    rows, K = _check_matrix("codes", codes, torch.int8)
-    if rows != M:
-        raise ValueError(f"codes has {rows} rows, dy {M}")
-    _check_plain("scales", scales, torch.float32, M)
-    dw = dy.new_empty((N, K)) if dw is None else dw
-    _check_plain("dw", dw, torch.bfloat16, N * K)
-    dev = _same_device(dy, codes=codes, scales=scales, dw=dw)
-    _check("wan_int8_grad_weight", lib().wan_int8_grad_weight(dy.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-                                                              dw.data_ptr(), M, N, K, _call_stream(dev)))
-    return dw
+    return _bound_call("int8_grad_weight", "wan_int8_grad_weight", dy, codes, scales, dw)
 
 
 def int8_grad_input(dy, w_codes, w_scales, dx=None, stream=None):
     """bf16 dX [M, K] = dY (w_codes * w_scales) from dY [M, N] and the weight's 8-bit codes
     (``wan_int8_grad_input``)."""
-    if torch is None:
-        _need_torch()
-    if stream is not None:             # what the call allocates then belongs to that stream too
-        with torch.cuda.stream(stream):
+    if stream is not None:
+        with _on(stream):
             return int8_grad_input(dy, w_codes, w_scales, dx)
-    M, N = _check_matrix("dy", dy, torch.bfloat16)
-    rows, K = _check_matrix("w_codes", w_codes, torch.int8)
-    if rows != N:
-        raise ValueError(f"w_codes has {rows} rows, dy {N} columns")
-    _check_plain("w_scales", w_scales, torch.float32, N)
-    dx = dy.new_empty((M, K)) if dx is None else dx
-    _check_plain("dx", dx, torch.bfloat16, M * K)
-    dev = _same_device(dy, w_codes=w_codes, w_scales=w_scales, dx=dx)
-    _check("wan_int8_grad_input", lib().wan_int8_grad_input(dy.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
-                                                            dx.data_ptr(), M, N, K, _call_stream(dev)))
-    return dx
+    return _bound_call("int8_grad_input", "wan_int8_grad_input", dy, w_codes, w_scales, dx)
 
 
 def fwd_q8_workspace_size(B, S, H, D=128) -> int:
