@@ -137,6 +137,7 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     const int warp = warp_id();
     const int lane = lane_id();
     const int hk = blockIdx.x % p.Hkv, group = p.H / p.Hkv;
+    grid_dependency_wait();
     const int2 at = p.order[blockIdx.x / p.Hkv];          // sequence, key tile
     if (at.x < 0) return;                                 // the grid is an upper bound
     const Span sq = span_of(p.cu_q, at.x, p.Tq), sk = span_of(p.cu_k, at.x, p.Tk);
@@ -187,6 +188,7 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_launch_dependents();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
 
     if (warp == WARP_TMA) {
@@ -624,6 +626,8 @@ __device__ void sort_tiles(const VarlenBwdParams& p) {
 // D_i = sum_d dO_id * O_id (fp32) for every (token, head) row, and dQ accumulator := 0.
 // 16 threads per row, 8 elements (16 bytes) each.  The first block sorts the key tiles instead.
 __global__ void __launch_bounds__(256) varlen_prep_kernel(const VarlenBwdParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     if (blockIdx.x == 0) {
         sort_tiles(p);
         return;
@@ -666,9 +670,10 @@ __global__ void __launch_bounds__(256) varlen_prep_kernel(const VarlenBwdParams 
 
 // out[t, h, :] = bf16(acc[t, h, :] * scale) for the tokens from the first sequence's to the last's,
 // 8 elements per thread; out has token stride ld.
-__global__ void __launch_bounds__(256) varlen_cast_kernel(const float* __restrict__ acc, __nv_bfloat16* __restrict__ out,
-                                                          const int* __restrict__ cu, int N, int T, int H, long long ld,
+__global__ void __launch_bounds__(256) varlen_cast_kernel(const float* acc, __nv_bfloat16* out, const int* cu, int N, int T, int H, long long ld,
                                                           float scale) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     const long long row8 = static_cast<long long>(H) * 16;                // 8-element parts to a token
     const long long begin = min(max(cu[0], 0), T) * row8, end = min(max(cu[N], 0), T) * row8;
     const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
@@ -728,8 +733,11 @@ int launch_varlen_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
                       cudaStream_t stream) {
     using namespace varlen_bwd;
     const int blocks = 148 * 8;          // grid-stride elementwise kernels: 8 blocks of 256 per SM
-    varlen_prep_kernel<<<1 + blocks, 256, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return -1;
+    auto cast = [&](const float* acc, void* out, const int* cu, int T, int heads, long long ld, float scale) {
+        return launch_dependent(varlen_cast_kernel, dim3(blocks), 256, 0, stream, 1, acc, static_cast<__nv_bfloat16*>(out), cu,
+                                p.N, T, heads, ld, scale);
+    };
+    if (launch_dependent(varlen_prep_kernel, dim3(1 + blocks), 256, 0, stream, 1, p) != 0) return -1;
     if (p.Tk > 0) {
         if (p.splits > 1) {
             const size_t bytes = static_cast<size_t>(p.Tk) * p.Hkv * HD * 4;
@@ -739,19 +747,13 @@ int launch_varlen_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
         }
         if (configure_smem(reinterpret_cast<const void*>(varlen_main_kernel), SMEM_BYTES) != 0) return -1;
         const dim3 grid(static_cast<unsigned>(p.tile_bound) * p.Hkv, 1, p.splits);
-        varlen_main_kernel<<<grid, NTHREADS, SMEM_BYTES, stream>>>(tq, tk, tv, tdo, tdq, tdk, tdv, p);
-        if (cudaGetLastError() != cudaSuccess) return -1;
-        if (p.splits > 1) {
-            varlen_cast_kernel<<<blocks, 256, 0, stream>>>(p.dk_acc, static_cast<__nv_bfloat16*>(p.dk), p.cu_k, p.N, p.Tk,
-                                                           p.Hkv, p.lddk, p.scale);
-            varlen_cast_kernel<<<blocks, 256, 0, stream>>>(p.dv_acc, static_cast<__nv_bfloat16*>(p.dv), p.cu_k, p.N, p.Tk,
-                                                           p.Hkv, p.lddv, 1.f);
-        }
+        if (launch_dependent(varlen_main_kernel, grid, NTHREADS, SMEM_BYTES, stream, 1, tq, tk, tv, tdo, tdq, tdk, tdv, p) != 0)
+            return -1;
+        if (p.splits > 1 && (cast(p.dk_acc, p.dk, p.cu_k, p.Tk, p.Hkv, p.lddk, p.scale) != 0 ||
+                             cast(p.dv_acc, p.dv, p.cu_k, p.Tk, p.Hkv, p.lddv, 1.f) != 0))
+            return -1;
     }
-    if (p.Tq > 0)
-        varlen_cast_kernel<<<blocks, 256, 0, stream>>>(p.dq_acc, static_cast<__nv_bfloat16*>(p.dq), p.cu_q, p.N, p.Tq, p.H,
-                                                       p.lddq, p.scale);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    return p.Tq > 0 ? cast(p.dq_acc, p.dq, p.cu_q, p.Tq, p.H, p.lddq, p.scale) : 0;
 }
 
 }  // namespace wan

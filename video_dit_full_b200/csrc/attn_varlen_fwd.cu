@@ -154,6 +154,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         *abort_flag = 0;
         fence_barrier_init();
     }
+    grid_dependency_wait();
     if (warp == WARP_MMA) {
         tmem_alloc(base + OFF_TMEM_SLOT, TMEM_COLS);
         tmem_relinquish();
@@ -161,6 +162,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_launch_dependents();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
 
     // Registers: the softmax warps hold a row's 128 scores; the launch's 384 x 168 are shared out as
@@ -643,6 +645,8 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
 // o = sum_z 2^(lse_z - lse) o_z, lse = log2 sum_z 2^lse_z over the splits' partial results: one warp per
 // (token, head) row.  The partial results are few (only calls with few query rows are split).
 __global__ void __launch_bounds__(128) varlen_join_kernel(const VarlenFwdParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     const long long rows = static_cast<long long>(p.Tq) * p.H;
     const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     if (row >= rows) return;
@@ -702,14 +706,12 @@ int launch_varlen_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
                       const VarlenFwdParams& p, cudaStream_t stream) {
     if (configure_smem(reinterpret_cast<const void*>(varlen::varlen_fwd_kernel), varlen::SMEM_BYTES) != 0) return -1;
     const dim3 grid(static_cast<unsigned>(varlen::tile_bound(p.N, p.Tq, p.pack) * (p.H / p.pack)), p.splits);
-    varlen::varlen_fwd_kernel<<<grid, varlen::NTHREADS, varlen::SMEM_BYTES, stream>>>(tq, tk, tv, to, p);
-    if (cudaGetLastError() != cudaSuccess) return -1;
-    if (p.splits > 1) {
-        const long long rows = static_cast<long long>(p.Tq) * p.H;
-        varlen::varlen_join_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p);
-        if (cudaGetLastError() != cudaSuccess) return -1;
-    }
-    return 0;
+    if (launch_dependent(varlen::varlen_fwd_kernel, grid, varlen::NTHREADS, varlen::SMEM_BYTES, stream, 1, tq, tk, tv, to,
+                         p) != 0)
+        return -1;
+    if (p.splits == 1) return 0;
+    const long long rows = static_cast<long long>(p.Tq) * p.H;
+    return launch_dependent(varlen::varlen_join_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, stream, 1, p);
 }
 
 }  // namespace wan

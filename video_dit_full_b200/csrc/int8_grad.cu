@@ -178,6 +178,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_y, const CUtens
         *abort_flag = 0;
         fence_barrier_init();
     }
+    grid_dependency_wait();
     if (warp == 1) {
         if (PAIR) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + OFF_TMEM_SLOT),
@@ -193,6 +194,7 @@ __device__ __forceinline__ void grad_body(const CUtensorMap& tma_y, const CUtens
     if (PAIR) cluster_sync_all();       // both CTAs' barriers and TMEM exist before any remote use
     else __syncthreads();
     tc_fence_after();
+    grid_launch_dependents();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
 
     if (warp == 0) {
@@ -476,27 +478,16 @@ int launch(const CUtensorMap& ta, const CUtensorMap& tc, const Params& p, cudaSt
     // reads twice the shared memory per product)
     if (static_cast<double>((t256 + 73) / 74) <= 0.5 / 0.7 * static_cast<double>((t128 + 147) / 148)) {
         if (configure_smem(reinterpret_cast<const void*>(grad_pair_kernel<Y_MN>), SMEM_BYTES) != 0) return -1;
-        grad_pair_kernel<Y_MN><<<2 * static_cast<unsigned>(t256 < 74 ? t256 : 74), NTHREADS, SMEM_BYTES, stream>>>(ta, tc, p);
-        return cudaGetLastError() == cudaSuccess ? 0 : -1;
+        return launch_dependent(grad_pair_kernel<Y_MN>, dim3(2 * static_cast<unsigned>(t256 < 74 ? t256 : 74)), NTHREADS,
+                                SMEM_BYTES, stream, 1, ta, tc, p);
     }
     if (configure_smem(reinterpret_cast<const void*>(grad_split_kernel<Y_MN>), SMEM_BYTES) != 0) return -1;
     // the terms are split while that still fits one CTA per SM and each has eight stages or more
     const int nk = (p.terms + BT - 1) / BT;
     int splits = 1;
     while (splits < 8 && (splits + 1) * t128 <= 148 && nk / (splits + 1) >= 8) ++splits;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(splits, static_cast<unsigned>(t128 < 65535 ? t128 : 65535), static_cast<unsigned>((t128 + 65534) / 65535));
-    cfg.blockDim = dim3(NTHREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, grad_split_kernel<Y_MN>, ta, tc, p) == cudaSuccess ? 0 : -1;
+    const dim3 grid(splits, static_cast<unsigned>(t128 < 65535 ? t128 : 65535), static_cast<unsigned>((t128 + 65534) / 65535));
+    return launch_dependent(grad_split_kernel<Y_MN>, grid, NTHREADS, SMEM_BYTES, stream, splits, ta, tc, p);
 }
 
 }  // namespace int8_grad

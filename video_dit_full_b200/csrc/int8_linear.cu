@@ -64,8 +64,8 @@ struct RowScale {
 // (rows of up to 8 CACHED T elements stay in registers between the absmax and the codes), the codes written
 // once.
 template <int T, int CACHED>
-__global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16* __restrict__ x, int8_t* __restrict__ codes,
-                                                         float* __restrict__ scales, int M, int K, long long ldx) {
+__global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16* x, int8_t* codes, float* scales, int M, int K, long long ldx) {
+    grid_dependency_wait();
     grid_launch_dependents();                              // a layer's product may fetch its weight meanwhile
     __shared__ uint32_t top[8];
     const int tid = threadIdx.x % T;
@@ -109,8 +109,9 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16* __
 // T threads per row, 256 / T rows per block, 8 codes per thread and step (a warp's store is 512 bytes in one
 // piece), eight steps' codes in flight.  Bound by memory.
 template <int T>
-__global__ void __launch_bounds__(256) dequant_rows_kernel(const uint2* __restrict__ codes, const float* __restrict__ scales,
-                                                           uint4* __restrict__ x, int M, int K8) {
+__global__ void __launch_bounds__(256) dequant_rows_kernel(const uint2* codes, const float* scales, uint4* x, int M, int K8) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     const long long m = static_cast<long long>(blockIdx.x) * (256 / T) + threadIdx.x / T;
     if (m >= M) return;
     const float s = scales[m];
@@ -214,6 +215,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constan
         *abort_flag = 0;
         fence_barrier_init();
     }
+    grid_dependency_wait();
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + OFF_TMEM_SLOT),
                      "r"(TMEM_COLS)
@@ -223,6 +225,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constan
     tc_fence_before();
     cluster_sync_all();                 // both CTAs' barriers and TMEM exist before any remote use
     tc_fence_after();
+    grid_launch_dependents();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
 
     if (warp == 0) {
@@ -447,6 +450,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant
         *abort_flag = 0;
         fence_barrier_init();
     }
+    if (!p.after_quant) grid_dependency_wait();
     if (warp == 1) {
         tmem_alloc(base + C::OFF_TMEM_SLOT, C::TMEM_COLS);
         tmem_relinquish();
@@ -454,6 +458,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_launch_dependents();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TMEM_SLOT);
 
     if (warp == 0) {
@@ -603,13 +608,15 @@ layer_few_kernel(const __grid_constant__ CUtensorMap tma_w, const LayerParams p)
         mbar_init(bar(C::DONE), 1);
         *abort_flag = 0;
         fence_barrier_init();
-        // the weight needs nothing of what follows
         tma_prefetch_desc(&tma_w);
+        // the weight needs nothing of what follows
+        grid_dependency_wait();
         for (int kb = 0; kb < min(nk, C::STAGES); ++kb) {
             mbar_arrive_expect_tx(bar(C::FULL + kb), C::A_BYTES);
             tma_load_2d(base + kb * C::A_BYTES, &tma_w, bar(C::FULL + kb), (k0 + kb) * BK, n0);
         }
     }
+    grid_dependency_wait();
     if (warp == 1) {
         tmem_alloc(base + C::OFF_TMEM_SLOT, C::TMEM_COLS);
         tmem_relinquish();
@@ -652,6 +659,7 @@ layer_few_kernel(const __grid_constant__ CUtensorMap tma_w, const LayerParams p)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_launch_dependents();
     if (warp >= 2) {
 #pragma unroll
         for (int i = 0; i < LAYER_PIECES; ++i) {
@@ -781,19 +789,8 @@ bool layer_fits(int M, int N, int K) {
 int launch_layer(const CUtensorMap& tw, const LayerParams& p, cudaStream_t stream) {
     if (configure_smem(reinterpret_cast<const void*>(layer_few_kernel), LayerCfg::SMEM_BYTES) != 0) return -1;
     const int splits = splits_for(1, p.N, p.K);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(splits, (p.N + 127) / 128);
-    cfg.blockDim = dim3(LayerCfg::NTHREADS);
-    cfg.dynamicSmemBytes = LayerCfg::SMEM_BYTES;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, layer_few_kernel, tw, p) == cudaSuccess ? 0 : -1;
+    return launch_dependent(layer_few_kernel, dim3(splits, (p.N + 127) / 128), LayerCfg::NTHREADS, LayerCfg::SMEM_BYTES,
+                            stream, splits, tw, p);
 }
 
 template <int NT>
@@ -801,55 +798,40 @@ int launch(const CUtensorMap& tx, const CUtensorMap& tw, const Int8GemmParams& p
     if (configure_smem(reinterpret_cast<const void*>(gemm_few_kernel<NT>), Cfg<NT>::SMEM_BYTES) != 0) return -1;
     const int n_tiles = (p.N + 127) / 128, m_tiles = (p.M + NT - 1) / NT;
     const int splits = splits_for(m_tiles, p.N, p.K);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(splits, n_tiles, m_tiles);
-    cfg.blockDim = dim3(NTHREADS);
-    cfg.dynamicSmemBytes = Cfg<NT>::SMEM_BYTES;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.after_quant ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, gemm_few_kernel<NT>, tx, tw, p) == cudaSuccess ? 0 : -1;
+    return launch_dependent(gemm_few_kernel<NT>, dim3(splits, n_tiles, m_tiles), NTHREADS, Cfg<NT>::SMEM_BYTES, stream,
+                            splits, tx, tw, p);
 }
 }  // namespace few
 
 template <int T, int CACHED>
-void launch_quant(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream) {
+int launch_quant(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream) {
     const int rows = 256 / T;
-    quant_rows_kernel<T, CACHED><<<(M + rows - 1) / rows, 256, 0, stream>>>(
-        static_cast<const __nv_bfloat16*>(x), static_cast<int8_t*>(codes), scales, M, K, ldx);
+    return launch_dependent(quant_rows_kernel<T, CACHED>, dim3((M + rows - 1) / rows), 256, 0, stream, 1,
+                            static_cast<const __nv_bfloat16*>(x), static_cast<int8_t*>(codes), scales, M, K, ldx);
 }
 template <int T>
-void launch_dequant(const void* codes, const float* scales, void* x, int M, int K, cudaStream_t stream) {
+int launch_dequant(const void* codes, const float* scales, void* x, int M, int K, cudaStream_t stream) {
     const int rows = 256 / T;
-    dequant_rows_kernel<T><<<(M + rows - 1) / rows, 256, 0, stream>>>(static_cast<const uint2*>(codes), scales,
-                                                                      static_cast<uint4*>(x), M, K / 8);
+    return launch_dependent(dequant_rows_kernel<T>, dim3((M + rows - 1) / rows), 256, 0, stream, 1,
+                            static_cast<const uint2*>(codes), scales, static_cast<uint4*>(x), M, K / 8);
 }
 
 }  // namespace int8
 
 int launch_int8_quant_rows(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream) {
     // few rows: all of a block on each, for latency; else as few threads as keep the row in registers
-    if (M <= 148) int8::launch_quant<256, 4>(x, codes, scales, M, K, ldx, stream);
-    else if (K <= 1024) int8::launch_quant<32, 4>(x, codes, scales, M, K, ldx, stream);
-    else if (K <= 2048) int8::launch_quant<32, 8>(x, codes, scales, M, K, ldx, stream);
-    else if (K <= 4096) int8::launch_quant<64, 8>(x, codes, scales, M, K, ldx, stream);
-    else if (K <= 8192) int8::launch_quant<128, 8>(x, codes, scales, M, K, ldx, stream);
-    else int8::launch_quant<256, 8>(x, codes, scales, M, K, ldx, stream);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    if (M <= 148) return int8::launch_quant<256, 4>(x, codes, scales, M, K, ldx, stream);
+    if (K <= 1024) return int8::launch_quant<32, 4>(x, codes, scales, M, K, ldx, stream);
+    if (K <= 2048) return int8::launch_quant<32, 8>(x, codes, scales, M, K, ldx, stream);
+    if (K <= 4096) return int8::launch_quant<64, 8>(x, codes, scales, M, K, ldx, stream);
+    if (K <= 8192) return int8::launch_quant<128, 8>(x, codes, scales, M, K, ldx, stream);
+    return int8::launch_quant<256, 8>(x, codes, scales, M, K, ldx, stream);
 }
 
 int launch_int8_dequant_rows(const void* codes, const float* scales, void* x, int M, int K, cudaStream_t stream) {
-    if (K <= 2048) int8::launch_dequant<32>(codes, scales, x, M, K, stream);
-    else if (K <= 8192) int8::launch_dequant<64>(codes, scales, x, M, K, stream);
-    else int8::launch_dequant<256>(codes, scales, x, M, K, stream);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    if (K <= 2048) return int8::launch_dequant<32>(codes, scales, x, M, K, stream);
+    if (K <= 8192) return int8::launch_dequant<64>(codes, scales, x, M, K, stream);
+    return int8::launch_dequant<256>(codes, scales, x, M, K, stream);
 }
 
 bool int8_layer_fits(int M, int N, int K) { return int8::few::layer_fits(M, N, K); }
@@ -883,8 +865,7 @@ int launch_int8_gemm(const CUtensorMap& tx, const CUtensorMap& tw, const Int8Gem
     if (configure_smem(reinterpret_cast<const void*>(pr::gemm_pair_kernel), pr::SMEM_BYTES) != 0) return -1;
     const long long tiles = static_cast<long long>((p.M + 255) / 256) * ((p.N + pr::BN - 1) / pr::BN);
     const int grid = 2 * static_cast<int>(tiles < 74 ? tiles : 74);
-    pr::gemm_pair_kernel<<<grid, int8::NTHREADS, pr::SMEM_BYTES, stream>>>(tx, tw, p);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    return launch_dependent(pr::gemm_pair_kernel, dim3(grid), int8::NTHREADS, pr::SMEM_BYTES, stream, 1, tx, tw, p);
 }
 
 }  // namespace wan

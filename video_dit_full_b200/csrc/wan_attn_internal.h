@@ -122,6 +122,32 @@ unsigned long long wait_budget_ns();
 // Sets the dynamic shared-memory limit of a kernel once per device.  0 on success.
 int configure_smem(const void* kernel, int bytes);
 
+// Launches a kernel that starts while the stream's kernel before it may still run (programmatic dependent
+// launch), `cluster` CTAs along x to a cluster.  What its CTAs set up before grid_dependency_wait overlaps
+// that kernel's end; nothing that kernel may have written is read before it (and no pointer is __restrict__,
+// which would let the compiler move a load of const data there).  Such a kernel allocates TMEM
+// only behind that wait (a waiting CTA then holds none that the kernel before it still has to get), and lets
+// the next one start, by grid_launch_dependents, only once it has it.
+template <typename... P, typename... A>
+int launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, int cluster,
+                     A&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...) == cudaSuccess ? 0 : -1;
+}
+
 // `to`: a map over O with the layout and box of tq (the epilogue TMA-stores O through it).
 int launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
                const FwdParams& p, cudaStream_t stream);
