@@ -174,12 +174,13 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         const int packed_heads = p.H / p.pack;
         int x = blockIdx.x, z = blockIdx.y;
         uint32_t asked = 0, item = 0;
-        ScanFrom from;
+        TileScan scan;
         bool more = true, pending = false;
         while (more) {
-            const TileAt at = tile_at(p.cu_q, p.N, p.Tq, 2 * tile_tokens, x / packed_heads, from);
+            const int tile = x / packed_heads;
+            const TileAt at = tile_at(p.cu_q, p.cu_k, p.N, p.Tq, p.Tk, 2 * tile_tokens, tile, scan);
             if (at.seq >= 0) {                        // the grid is an upper bound
-                const Span sq = span_of(p.cu_q, at.seq, p.Tq), sk = span_of(p.cu_k, at.seq, p.Tk);
+                const Span sq = at.q, sk = at.k;
                 const int i0 = (at.tiles - 1 - at.tile) * 2 * tile_tokens;
                 const int shift = sk.len - sq.len;    // causal: token i sees keys 0 .. i + shift
                 int nblk[2];                          // key blocks that tile t needs (its last token sees the most)
@@ -203,7 +204,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                     w->nt[1] = shared ? n / 2 : min(max(nblk[1] - j0, 0), n);
                     w->shared = shared ? 1 : 0;
                     w->j0 = j0;
-                    w->h0 = x % packed_heads * p.pack;
+                    w->h0 = (x - tile * packed_heads) * p.pack;
                     w->q_begin = sq.begin;
                     w->q_len = sq.len;
                     w->k_begin = sk.begin;
