@@ -264,6 +264,40 @@ def test_nan_shows(lens_q, lens_k, H, Hkv):
     wa.check_status()
 
 
+SPLIT = {
+    "mixed": ([1] * 9, [9000, 20, 0, 300, 4000, 17, 800, 128, 1], 8, 2, True),
+    "most_parts": ([1], [40000], 2, 1, True),
+    "more_items_than_estimated": ([300, 0, 0], [20000, 5, 0], 1, 1, True),
+    "more_items_than_estimated_full": ([300, 0, 0], [20000, 5, 0], 1, 1, False),
+    "few_rows_full": ([5, 40, 1], [3000, 9000, 1], 4, 4, False),
+    "more_queries_than_keys": ([40, 30], [20, 7000], 4, 2, True),
+    "sixty": ([1] * 60, [(37 * i * i) % 1500 for i in range(60)], 6, 2, True),
+}
+
+
+@pytest.mark.parametrize("case", SPLIT)
+def test_split_keys(case):
+    """Calls whose keys go to several work items: rows before and behind the sequences stay as they were."""
+    import torch
+    import video_dit_full_b200 as wa
+    lens_q, lens_k, H, Hkv, causal = SPLIT[case]
+    x, cu_q, cu_k = make(lens_q, lens_k, H, Hkv, seed=12, before=3, after=5)
+    d, cq, ck = dev(x, cu_q, cu_k)
+    T = d["q"].shape[0]
+    assert wa.varlen_fwd_workspace_size(len(lens_q), T, d["k"].shape[0], H, Hkv) > 0
+    o = torch.full((T, H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((H, T), 7.0, device="cuda")
+    wa.varlen_fwd(d["q"], d["k"], d["v"], cq, ck, causal=causal, o=o, lse=lse)
+    wa.check_status()
+    for n in range(T):
+        if n < 3 or n >= T - 5:
+            assert (o[n] == 7).all() and (lse[:, n] == 7).all()
+    again = wa.varlen_fwd(d["q"], d["k"], d["v"], cq, ck, causal=causal)[0]
+    assert torch.equal(again[3:T - 5], o[3:T - 5])
+    _, _, grads = run(d, cq, ck, causal)
+    compare(x, cu_q, cu_k, causal, o, lse, grads)
+
+
 def test_many_sequences():
     import video_dit_full_b200 as wa
     rng = np.random.default_rng(0)

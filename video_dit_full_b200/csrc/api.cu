@@ -781,11 +781,10 @@ int wan_fp8_gemm(const void* a_codes, const float* a_scales, const void* b_codes
 
 size_t wan_attn_varlen_fwd_workspace_size(int N, int Tq, int Tk, int H, int Hkv, int D) {
     if (check_packed(N, Tq, Tk, H, Hkv, D) != WAN_ATTN_OK) return 0;
-    int pack, splits;
-    varlen_fwd_plan(N, Tq, Tk, H, Hkv, &pack, &splits);
-    if (splits == 1) return 0;
-    const size_t rows = size_t(splits) * Tq * H;
-    return align256(rows * 128 * 4) + align256(rows * 4);
+    const VarlenFwdPlan plan = varlen_fwd_plan(N, Tq, Tk, H, Hkv);
+    if (plan.chunk == 0) return 0;
+    const size_t rows = size_t(plan.parts) * Tq * H;
+    return align256(rows * 128 * 4) + align256(rows * 4) + align256(size_t(Tq) * 4);
 }
 
 int wan_attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, float* lse, const int* cu_q,
@@ -809,11 +808,16 @@ int wan_attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, fl
     if (!fill_packed(p, q, k, v, cu_q, cu_k, N, Tq, Tk, H, Hkv, ldq, ldk, ldv, causal)) return WAN_ATTN_ERR_CUDA;
     p.o = o;
     p.lse = lse;
-    varlen_fwd_plan(N, Tq, Tk, H, Hkv, &p.pack, &p.splits);
+    const VarlenFwdPlan plan = varlen_fwd_plan(N, Tq, Tk, H, Hkv);
+    p.pack = plan.pack;
+    p.chunk = plan.chunk;
+    p.streamed = plan.streamed;
     if (need) {
-        p.o_part = static_cast<float*>(workspace);
-        p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                              align256(size_t(p.splits) * Tq * H * 128 * 4));
+        const size_t rows = size_t(plan.parts) * Tq * H;
+        char* ws = static_cast<char*>(workspace);
+        p.o_part = reinterpret_cast<float*>(ws);
+        p.lse_part = reinterpret_cast<float*>(ws + align256(rows * 128 * 4));
+        p.parts = reinterpret_cast<int*>(ws + align256(rows * 128 * 4) + align256(rows * 4));
     }
     CUtensorMap tq, tk, tv, to;
     if (!make_packed_map(&tq, q, Tq, H, ldq, p.pack, 128 / p.pack) ||
@@ -825,7 +829,7 @@ int wan_attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, fl
     } else {
         tk = tv = tq;                     // never read: without keys no tile has a key block
     }
-    return as_status(launch_varlen_fwd(tq, tk, tv, to, p, static_cast<cudaStream_t>(stream)));
+    return as_status(launch_varlen_fwd(tq, tk, tv, to, p, plan.units, static_cast<cudaStream_t>(stream)));
 }
 
 size_t wan_attn_varlen_bwd_workspace_size(int N, int Tq, int Tk, int H, int Hkv, int D) {

@@ -16,7 +16,7 @@
 // Items differ by orders of magnitude (a causal tile's keys, a sequence's length) and the short ones are
 // mostly prologue and epilogue, so a CTA goes on to another item without a break: the scheduler asks the
 // hardware for a block that has not started yet (cluster launch control), finds its place and its key
-// range by a scan over the offsets (tile_at: no table, no extra launch), and hands it to the other warps
+// range by a scan over the offsets (item_at: no table, no extra launch), and hands it to the other warps
 // through two slots, some key blocks before it is needed.  K and V of the next item load, and its first scores are computed,
 // under the epilogue of the last; the two tiles' groups run apart.  The grid is ordered head fastest and
 // a sequence's tiles backwards, so that causal's longest start first and neighbours are alike.
@@ -29,8 +29,9 @@
 //   - an item with a single Q tile (a generated token, a sequence's last rows) has both groups work on it,
 //     each on every other key block with a running m, l and O of its own, joined at the end in TMEM: one
 //     group alone would leave the memory idle between its scores and its products
-//   - few query rows against many keys: gridDim.y items split the keys and a second kernel joins their
-//     normalised fp32 partial results by their lse
+//   - few query rows against many keys: a sequence's keys go to several items, `chunk` key blocks to each, so
+//     that sequences of any lengths make items of one size, and a second kernel joins their normalised fp32
+//     partial results by their lse
 #include <cuda.h>
 
 #include "sm100_ptx.cuh"
@@ -50,6 +51,7 @@ constexpr int OFF_K = OFF_Q + 2 * TILE_BYTES;
 constexpr int OFF_V = OFF_K + 2 * TILE_BYTES;
 constexpr int OFF_WORK = OFF_V + 2 * TILE_BYTES;   // two work slots
 constexpr int WORK_BYTES = 64;
+constexpr int MAX_PARTS = 64;                      // of a sequence's keys
 constexpr int AHEAD = 6;                           // key blocks left of an item when the next one is fetched
 constexpr int OFF_CLC = OFF_WORK + 2 * WORK_BYTES; // cluster launch control's answer
 constexpr int OFF_ML = OFF_CLC + 16;               // m and l of tile 1's rows, for the join of a shared tile
@@ -74,7 +76,7 @@ struct Work {
     int q_begin, q_len;    // the sequence's rows on the query axis
     int k_begin, k_len;    // ... and on the key axis
     int i0;                // first token of the item, within the sequence
-    int split;
+    int part, parts;       // of the tile's keys
 };
 static_assert(sizeof(Work) <= WORK_BYTES, "a work slot");
 __device__ __forceinline__ int ld_shared_int(uint32_t addr) {
@@ -172,16 +174,28 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
     if (warp == WARP_SCHED) {
         // ------------------------------ scheduler ---------------------------------
         const int packed_heads = p.H / p.pack;
-        int x = blockIdx.x, z = blockIdx.y;
+        const int units = gridDim.x / packed_heads;
+        int x = blockIdx.x;
         uint32_t asked = 0, item = 0;
-        TileScan scan;
+        ItemScan scan;
         bool more = true, pending = false;
         while (more) {
-            const int tile = x / packed_heads;
-            const TileAt at = tile_at(p.cu_q, p.cu_k, p.N, p.Tq, p.Tk, 2 * tile_tokens, tile, scan);
-            if (at.seq >= 0) {                        // the grid is an upper bound
+            const int unit = x / packed_heads, h0 = (x - unit * packed_heads) * p.pack;
+            bool ok = true;
+            // a block stands for item `unit`; with split keys, where the grid is an estimate, also for every
+            // units-th one after it
+            for (int target = unit;; target += units) {
+                const ItemAt at = item_at(p.cu_q, p.cu_k, p.N, p.Tq, p.Tk, 2 * tile_tokens, p.chunk * BN, target, scan);
+                if (at.seq < 0) break;
                 const Span sq = at.q, sk = at.k;
-                const int i0 = (at.tiles - 1 - at.tile) * 2 * tile_tokens;
+                int tile = at.item, tiles = at.items, part = 0, parts = 1;
+                if (p.chunk) {
+                    parts = max(parts_of(sk.len, p.chunk * BN), 1);
+                    tile /= parts;
+                    tiles /= parts;
+                    part = at.item - tile * parts;
+                }
+                const int i0 = (tiles - 1 - tile) * 2 * tile_tokens;
                 const int shift = sk.len - sq.len;    // causal: token i sees keys 0 .. i + shift
                 int nblk[2];                          // key blocks that tile t needs (its last token sees the most)
 #pragma unroll
@@ -192,10 +206,10 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                     nblk[t] = (keys + BN - 1) / BN;
                 }
                 const int all = max(nblk[0], nblk[1]);
-                const int share = (all + p.splits - 1) / p.splits;
-                const int j0 = min(z * share, all);
-                const int n = min(share, all - j0);   // blocks j0 .. j0 + n - 1
-                if (!wait_item(bar(W_EMPTY + (item & 1u)), ((item >> 1) & 1u) ^ 1u, wc)) break;
+                const int j0 = min(part * p.chunk, all);
+                const int n = p.chunk ? min(p.chunk, all - j0) : all;   // blocks j0 .. j0 + n - 1
+                ok = wait_item(bar(W_EMPTY + (item & 1u)), ((item >> 1) & 1u) ^ 1u, wc);
+                if (!ok) break;
                 if (lane == 0) {
                     volatile Work* w = slot_of(item);
                     const bool shared = i0 + tile_tokens >= sq.len && n > 1;
@@ -204,20 +218,24 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                     w->nt[1] = shared ? n / 2 : min(max(nblk[1] - j0, 0), n);
                     w->shared = shared ? 1 : 0;
                     w->j0 = j0;
-                    w->h0 = (x - tile * packed_heads) * p.pack;
+                    w->h0 = h0;
                     w->q_begin = sq.begin;
                     w->q_len = sq.len;
                     w->k_begin = sk.begin;
                     w->k_len = sk.len;
                     w->i0 = i0;
-                    w->split = z;
+                    w->part = part;
+                    w->parts = parts;
                     mbar_arrive(bar(W_FULL + (item & 1u)));
                 }
                 // the producer says when this item nears its end: a block taken earlier could wait here while
                 // other SMs run out of work
-                if (!wait_item(bar(NEXT), item & 1u, wc)) break;
+                ok = wait_item(bar(NEXT), item & 1u, wc);
+                if (!ok) break;
                 ++item;
+                if (!p.chunk) break;
             }
+            if (!ok) break;
             pending = true;
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar(CLC), 16);
@@ -227,7 +245,8 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
             if (!wait_warp(bar(CLC), asked & 1u, wc)) break;
             pending = false;
             ++asked;
-            more = clc_answer(base + OFF_CLC, x, z);
+            int y;
+            more = clc_answer(base + OFF_CLC, x, y);
             fence_proxy_async_smem();                 // read before the next answer overwrites it
             __syncwarp();
         }
@@ -243,7 +262,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
             tma_prefetch_desc(&tmk);
             tma_prefetch_desc(&tmv);
         }
-        const uint64_t keep = l2_policy_evict_last();
+        const uint64_t keep = p.streamed ? l2_policy_evict_first() : l2_policy_evict_last();
         const uint32_t qbytes = static_cast<uint32_t>(p.pack * tile_tokens) * 256u;
         uint32_t kv = 0, tails = 0, loads[2] = {0, 0};     // K/V stages, V_TAIL phases and Q tiles used so far
         uint32_t k_out = 0, v_out = 0;                     // copies issued on K_FULL and V_FULL (the last two may be in flight)
@@ -555,7 +574,8 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
             const int head = WORK(w, h0) + r - row_tok * p.pack, token = WORK(w, q_begin) + i_tile + row_tok;
             const bool real = row_tok < tile_tokens && i_tile + row_tok < q_len && !(shared && t == 1);
             const bool empty = l == 0.f;                      // the row saw no key here (a NaN score leaves l NaN: it shows)
-            const bool by_tma = p.splits == 1 && i_tile + tile_tokens <= q_len && nt > 0 && !shared;
+            const bool split = WORK(w, parts) > 1;
+            const bool by_tma = !split && i_tile + tile_tokens <= q_len && nt > 0 && !shared;
             const uint32_t stage = sQ + t * TILE_BYTES;
             if (ok && !(shared && t == 1)) {
                 tc_fence_after();
@@ -563,7 +583,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                 a0 *= inv_l;
                 a1 *= inv_l;
                 const long long row = static_cast<long long>(token) * p.H + head;
-                const long long part = static_cast<long long>(WORK(w, split)) * p.Tq * p.H;
+                const long long part = static_cast<long long>(WORK(w, part)) * p.Tq * p.H;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {                 // 32 columns of d at a time
                     uint32_t o[32];
@@ -581,7 +601,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                         for (int e = 0; e < 32; ++e)
                             if (a1 != 0.f) o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), a1, __uint_as_float(o[e])));
                     }
-                    if (p.splits > 1) {
+                    if (split) {
                         if (real && !empty) {
                             uint4* dst = reinterpret_cast<uint4*>(p.o_part + (part + row) * HD + q * 32);
 #pragma unroll
@@ -615,7 +635,8 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
                 if (real) {
                     const float lse2 = empty ? -INFINITY : m_ref + log2f(l);
                     const long long at = static_cast<long long>(head) * p.Tq + token;
-                    if (p.splits > 1) p.lse_part[part + at] = lse2;
+                    if (p.chunk && head == 0 && WORK(w, part) == 0) p.parts[token] = WORK(w, parts);
+                    if (split) p.lse_part[part + at] = lse2;
                     else p.lse[at] = lse2 * 0.69314718055994531f;
                 }
             }
@@ -643,8 +664,8 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
     if (warp == WARP_MMA) tmem_dealloc(tmem, TMEM_COLS);
 }
 
-// o = sum_z 2^(lse_z - lse) o_z, lse = log2 sum_z 2^lse_z over the splits' partial results: one warp per
-// (token, head) row.  The partial results are few (only calls with few query rows are split).
+// o = sum_z 2^(lse_z - lse) o_z, lse = log2 sum_z 2^lse_z over the parts' results: one warp per (token, head)
+// row.  They are few (only calls with few query rows are split).
 __global__ void __launch_bounds__(128) varlen_join_kernel(const VarlenFwdParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -653,18 +674,35 @@ __global__ void __launch_bounds__(128) varlen_join_kernel(const VarlenFwdParams 
     if (row >= rows) return;
     const int lane = threadIdx.x & 31, token = static_cast<int>(row / p.H), head = static_cast<int>(row % p.H);
     if (token < p.cu_q[0] || token >= p.cu_q[p.N]) return;       // outside every sequence
+    const int parts = p.parts[token];
+    if (parts == 1) return;                                      // the item wrote its results itself
+    // the parts' weights: part z and z + 32 in lane z, then one after the other past every lane's columns
     const float* lse = p.lse_part + static_cast<long long>(head) * p.Tq + token;
-    float m = -INFINITY;
-    for (int z = 0; z < p.splits; ++z) m = fmaxf(m, lse[z * rows]);
+    static_assert(MAX_PARTS == 64, "two parts to a lane");
+    const float z0 = lane < parts ? lse[lane * rows] : -INFINITY, z1 = lane + 32 < parts ? lse[(lane + 32) * rows] : -INFINITY;
+    float m = fmaxf(z0, z1);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float w0 = z0 == -INFINITY ? 0.f : ex2_approx(z0 - m), w1 = z1 == -INFINITY ? 0.f : ex2_approx(z1 - m);
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int z = 0; z < p.splits; ++z) {
-        const float lz = lse[z * rows];
-        if (lz == -INFINITY) continue;                // nothing was written there
-        const float w = ex2_approx(lz - m);
-        const float4 o = *reinterpret_cast<const float4*>(p.o_part + (z * rows + row) * HD + lane * 4);
-        l += w;
-        acc = make_float4(fmaf(w, o.x, acc.x), fmaf(w, o.y, acc.y), fmaf(w, o.z, acc.z), fmaf(w, o.w, acc.w));
+    const float* src = p.o_part + row * HD + lane * 4;
+    for (int g = 0; g < parts; g += 8) {
+        float w[8];
+        float4 o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            w[e] = __shfl_sync(0xffffffffu, g < 32 ? w0 : w1, (g + e) & 31);
+            // a part of weight 0 may not have been written
+            if (w[e] != 0.f) o[e] = *reinterpret_cast<const float4*>(src + (g + e) * rows * HD);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (w[e] == 0.f) continue;
+            l += w[e];
+            acc = make_float4(fmaf(w[e], o[e].x, acc.x), fmaf(w[e], o[e].y, acc.y), fmaf(w[e], o[e].z, acc.z),
+                              fmaf(w[e], o[e].w, acc.w));
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;       // a NaN shows
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * HD + lane * 4) =
@@ -684,33 +722,52 @@ static long long tile_bound(int N, int Tq, int pack) {
 }  // namespace varlen
 
 // pack: the most heads of a group that fill at least 120 of a tile's 128 rows (128 / pack tokens of
-// `pack` heads each).  splits: a tile's keys go to several items when there are fewer than two tiles for
-// every SM, enough to make two; and when the sequences are single tiles on average (generated tokens:
-// memory bound, lengths anything), enough to make eight, so that the longest sequence's items do not
-// outlast the rest.  An item keeps 4 key blocks on average.
-void varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv, int* pack, int* splits) {
+// `pack` heads each).
+// chunk: keys are split when there are fewer than two tiles for every SM, into parts that make two; and when
+// the sequences are single tiles on average (generated tokens: memory bound, lengths anything), into parts that
+// make four.  Parts of one size rather than a number of parts to each sequence: 40 generated tokens of 8 kv heads
+// against 17 to 9806 keys 152 us (5.3 TB/s) against 159, 8 of 4 kv heads against 11,089 keys, one of them 8650,
+// 25 us against 52.  A part has at least 4 blocks (its prologue and epilogue take as long as two or three), there
+// are at most 64, and the partial results take no more memory than K and V, or 16 MB.  Beyond SPLIT_N sequences
+// the scheduler's scan over the offsets would take longer than an item.
+VarlenFwdPlan varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv) {
+    constexpr int SPLIT_N = 256, MIN_CHUNK = 4;
     const int group = H / Hkv;
     int pk = 1;
     for (int d = 1; d <= group && d <= varlen::BM; ++d)
         if (group % d == 0 && (varlen::BM / d) * d >= 120) pk = d;
-    *pack = pk;
-    const long long ctas = varlen::tile_bound(N, Tq, pk) * (H / pk);
-    const long long blocks = (static_cast<long long>(Tk) / N + varlen::BN - 1) / varlen::BN;
-    const long long want = (static_cast<long long>(Tq) <= static_cast<long long>(N) * (varlen::BM / pk) ? 8 : 2) * 148;
-    long long s = ctas > 0 && ctas < want ? (want + ctas - 1) / ctas : 1;
-    if (s > blocks / 4) s = blocks / 4;
-    if (s > 64) s = 64;
-    *splits = s < 1 ? 1 : static_cast<int>(s);
+    const long long tiles = varlen::tile_bound(N, Tq, pk), ctas = tiles * (H / pk);
+    const long long blocks = (static_cast<long long>(Tk) + varlen::BN - 1) / varlen::BN;
+    const bool single = static_cast<long long>(Tq) <= static_cast<long long>(N) * (varlen::BM / pk);
+    VarlenFwdPlan plan{pk, 0, single ? 1 : 0, 1, tiles};
+    const long long want = (single ? 4 : 2) * 148;
+    if (ctas == 0 || ctas >= want || N > SPLIT_N) return plan;
+    // key blocks that one head's items walk in all: a sequence's once for every tile of its queries
+    const long long walked = single ? blocks : blocks * ((tiles + N - 1) / N);
+    const long long items = (want + H / pk - 1) / (H / pk);            // of one packed head
+    long long chunk = (walked + items - 1) / items;
+    if (chunk < MIN_CHUNK) chunk = MIN_CHUNK;
+    double memory = 256.0 * Tk * Hkv * 2;
+    if (memory < 16 << 20) memory = 16 << 20;
+    long long most = static_cast<long long>(memory / (516.0 * Tq * H));
+    if (most > varlen::MAX_PARTS) most = varlen::MAX_PARTS;
+    if (most < 2) return plan;
+    if (chunk < (blocks + most - 1) / most) chunk = (blocks + most - 1) / most;
+    if (blocks <= chunk) return plan;
+    plan.chunk = static_cast<int>(chunk);
+    plan.parts = static_cast<int>((blocks + chunk - 1) / chunk);
+    plan.units = walked / chunk + tiles;
+    return plan;
 }
 
 int launch_varlen_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
-                      const VarlenFwdParams& p, cudaStream_t stream) {
+                      const VarlenFwdParams& p, long long units, cudaStream_t stream) {
     if (configure_smem(reinterpret_cast<const void*>(varlen::varlen_fwd_kernel), varlen::SMEM_BYTES) != 0) return -1;
-    const dim3 grid(static_cast<unsigned>(varlen::tile_bound(p.N, p.Tq, p.pack) * (p.H / p.pack)), p.splits);
+    const dim3 grid(static_cast<unsigned>(units * (p.H / p.pack)));
     if (launch_dependent(varlen::varlen_fwd_kernel, grid, varlen::NTHREADS, varlen::SMEM_BYTES, stream, 1, tq, tk, tv, to,
                          p) != 0)
         return -1;
-    if (p.splits == 1) return 0;
+    if (!p.chunk) return 0;
     const long long rows = static_cast<long long>(p.Tq) * p.H;
     return launch_dependent(varlen::varlen_join_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, stream, 1, p);
 }

@@ -86,9 +86,11 @@ struct VarlenFwdParams : VarlenParams {
     void* o;                          // bf16 [Tq, H, 128]
     float* lse;                       // fp32 [H, Tq]
     int pack;                         // query heads that share a Q tile (a divisor of H / Hkv)
-    int splits;                       // CTAs among which a tile's keys are split
-    float* o_part;                    // workspace fp32 [splits, Tq, H, 128], splits > 1 only
-    float* lse_part;                  // workspace fp32 [splits, H, Tq] (base-2 log)
+    int chunk;                        // key blocks of a part where a sequence's keys are split, 0: they are not
+    int streamed;                     // K and V are read about once
+    float* o_part;                    // workspace fp32 [most parts, Tq, H, 128], where split
+    float* lse_part;                  // workspace fp32 [most parts, H, Tq] (base-2 log)
+    int* parts;                       // workspace [Tq]: parts of the token's sequence
 };
 struct VarlenBwdParams : VarlenParams {
     const void *o, *dout;             // bf16 [Tq, H, 128]
@@ -182,9 +184,14 @@ int launch_fp8_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensor
 // Packed attention (attn_varlen_fwd.cu, attn_varlen_bwd.cu).  0 on success.
 // tq, to: maps over q and o (128, H, Tq) with boxes (64, pack, 128 / pack); tk, tv: (128, Hkv, Tk), (64, 1, 128).
 int launch_varlen_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
-                      const VarlenFwdParams& p, cudaStream_t stream);
+                      const VarlenFwdParams& p, long long units, cudaStream_t stream);
 // How the forward lays out a call: heads per Q tile and splits of the keys (see VarlenFwdParams).
-void varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv, int* pack, int* splits);
+struct VarlenFwdPlan {
+    int pack, chunk, streamed;        // as in VarlenFwdParams
+    int parts;                        // most parts of a sequence
+    long long units;                  // the grid: units x (H / pack)
+};
+VarlenFwdPlan varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv);
 // tk, tv: boxes (64, 1, 128); tq, tdo: (64, pack, 128 / pack); tdq: fp32 [Tq, H, 128], (128, pack, 128 / pack); tdk, tdv: fp32
 // [Tk, Hkv, 128], boxes (32, 1, 128) with the 128-byte swizzle, only read when p.splits > 1.
 int launch_varlen_bwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
