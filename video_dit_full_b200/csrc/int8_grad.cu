@@ -479,7 +479,7 @@ int launch(const CUtensorMap& ta, const CUtensorMap& tc, const Params& p, cudaSt
     if (static_cast<double>((t256 + 73) / 74) <= 0.5 / 0.7 * static_cast<double>((t128 + 147) / 148)) {
         if (configure_smem(reinterpret_cast<const void*>(grad_pair_kernel<Y_MN>), SMEM_BYTES) != 0) return -1;
         return launch_dependent(grad_pair_kernel<Y_MN>, dim3(2 * static_cast<unsigned>(t256 < 74 ? t256 : 74)), NTHREADS,
-                                SMEM_BYTES, stream, 1, ta, tc, p);
+                                SMEM_BYTES, stream, 1, true, ta, tc, p);
     }
     if (configure_smem(reinterpret_cast<const void*>(grad_split_kernel<Y_MN>), SMEM_BYTES) != 0) return -1;
     // the terms are split while that still fits one CTA per SM and each has eight stages or more
@@ -487,7 +487,7 @@ int launch(const CUtensorMap& ta, const CUtensorMap& tc, const Params& p, cudaSt
     int splits = 1;
     while (splits < 8 && (splits + 1) * t128 <= 148 && nk / (splits + 1) >= 8) ++splits;
     const dim3 grid(splits, static_cast<unsigned>(t128 < 65535 ? t128 : 65535), static_cast<unsigned>((t128 + 65534) / 65535));
-    return launch_dependent(grad_split_kernel<Y_MN>, grid, NTHREADS, SMEM_BYTES, stream, splits, ta, tc, p);
+    return launch_dependent(grad_split_kernel<Y_MN>, grid, NTHREADS, SMEM_BYTES, stream, splits, true, ta, tc, p);
 }
 
 }  // namespace int8_grad

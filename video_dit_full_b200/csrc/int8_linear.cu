@@ -790,7 +790,7 @@ int launch_layer(const CUtensorMap& tw, const LayerParams& p, cudaStream_t strea
     if (configure_smem(reinterpret_cast<const void*>(layer_few_kernel), LayerCfg::SMEM_BYTES) != 0) return -1;
     const int splits = splits_for(1, p.N, p.K);
     return launch_dependent(layer_few_kernel, dim3(splits, (p.N + 127) / 128), LayerCfg::NTHREADS, LayerCfg::SMEM_BYTES,
-                            stream, splits, tw, p);
+                            stream, splits, true, tw, p);
 }
 
 template <int NT>
@@ -799,20 +799,20 @@ int launch(const CUtensorMap& tx, const CUtensorMap& tw, const Int8GemmParams& p
     const int n_tiles = (p.N + 127) / 128, m_tiles = (p.M + NT - 1) / NT;
     const int splits = splits_for(m_tiles, p.N, p.K);
     return launch_dependent(gemm_few_kernel<NT>, dim3(splits, n_tiles, m_tiles), NTHREADS, Cfg<NT>::SMEM_BYTES, stream,
-                            splits, tx, tw, p);
+                            splits, true, tx, tw, p);
 }
 }  // namespace few
 
 template <int T, int CACHED>
 int launch_quant(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream) {
     const int rows = 256 / T;
-    return launch_dependent(quant_rows_kernel<T, CACHED>, dim3((M + rows - 1) / rows), 256, 0, stream, 1,
+    return launch_dependent(quant_rows_kernel<T, CACHED>, dim3((M + rows - 1) / rows), 256, 0, stream, 1, true,
                             static_cast<const __nv_bfloat16*>(x), static_cast<int8_t*>(codes), scales, M, K, ldx);
 }
 template <int T>
 int launch_dequant(const void* codes, const float* scales, void* x, int M, int K, cudaStream_t stream) {
     const int rows = 256 / T;
-    return launch_dependent(dequant_rows_kernel<T>, dim3((M + rows - 1) / rows), 256, 0, stream, 1,
+    return launch_dependent(dequant_rows_kernel<T>, dim3((M + rows - 1) / rows), 256, 0, stream, 1, true,
                             static_cast<const uint2*>(codes), scales, static_cast<uint4*>(x), M, K / 8);
 }
 
@@ -865,7 +865,7 @@ int launch_int8_gemm(const CUtensorMap& tx, const CUtensorMap& tw, const Int8Gem
     if (configure_smem(reinterpret_cast<const void*>(pr::gemm_pair_kernel), pr::SMEM_BYTES) != 0) return -1;
     const long long tiles = static_cast<long long>((p.M + 255) / 256) * ((p.N + pr::BN - 1) / pr::BN);
     const int grid = 2 * static_cast<int>(tiles < 74 ? tiles : 74);
-    return launch_dependent(pr::gemm_pair_kernel, dim3(grid), int8::NTHREADS, pr::SMEM_BYTES, stream, 1, tx, tw, p);
+    return launch_dependent(pr::gemm_pair_kernel, dim3(grid), int8::NTHREADS, pr::SMEM_BYTES, stream, 1, true, tx, tw, p);
 }
 
 }  // namespace wan

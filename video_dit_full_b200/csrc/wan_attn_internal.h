@@ -130,8 +130,9 @@ int configure_smem(const void* kernel, int bytes);
 // which would let the compiler move a load of const data there).  Such a kernel allocates TMEM
 // only behind that wait (a waiting CTA then holds none that the kernel before it still has to get), and lets
 // the next one start, by grid_launch_dependents, only once it has it.
+// `early` false: an ordinary launch.
 template <typename... P, typename... A>
-int launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, int cluster,
+int launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, int cluster, bool early,
                      A&&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
@@ -140,7 +141,7 @@ int launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cud
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = early ? 1 : 0;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = 1;
