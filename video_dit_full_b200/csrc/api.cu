@@ -812,6 +812,7 @@ int wan_attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, fl
     p.pack = plan.pack;
     p.chunk = plan.chunk;
     p.streamed = plan.streamed;
+    p.order = plan.order;
     if (need) {
         const size_t rows = size_t(plan.parts) * Tq * H;
         char* ws = static_cast<char*>(workspace);
@@ -875,6 +876,7 @@ int wan_attn_varlen_bwd(const void* q, const void* k, const void* v, const void*
     p.splits = varlen_bwd_splits(N, Tq, Tk, H, Hkv);
     char* ws = static_cast<char*>(workspace);
     p.tile_bound = varlen_bwd_tile_bound(N, Tk);
+    if (Tk > 0) p.heads = head_order(p.tile_bound, Hkv, 1024.0 * Tq * H);       // Q, dO and the fp32 dQ
     const int pack = varlen_bwd_pack(H, Hkv);
     while ((1 << p.pack_log2) < pack) ++p.pack_log2;
     const size_t off_delta = align256(size_t(Tq) * H * 128 * 4), off_order = off_delta + align256(size_t(Tq) * H * 4);

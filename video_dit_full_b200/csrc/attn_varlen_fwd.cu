@@ -18,8 +18,9 @@
 // hardware for a block that has not started yet (cluster launch control), finds its place and its key
 // range by a scan over the offsets (item_at: no table, no extra launch), and hands it to the other warps
 // through two slots, some key blocks before it is needed.  K and V of the next item load, and its first scores are computed,
-// under the epilogue of the last; the two tiles' groups run apart.  The grid is ordered head fastest and
-// a sequence's tiles backwards, so that causal's longest start first and neighbours are alike.
+// under the epilogue of the last; the two tiles' groups run apart.  A sequence's tiles go backwards, so that
+// causal's longest start first, and heads in groups (HeadOrder): 16384 tokens of 40 heads, causal, 2.50 ms
+// against 2.61 with all heads in turn.
 // What packing sequences adds:
 //   - each tile has its own last key block (causal), blocks behind the diagonal are never loaded, and
 //     only blocks on the diagonal or at the sequence's end are masked (a count per row)
@@ -173,14 +174,15 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == WARP_SCHED) {
         // ------------------------------ scheduler ---------------------------------
-        const int packed_heads = p.H / p.pack;
-        const int units = gridDim.x / packed_heads;
+        const int units = p.order.units;
         int x = blockIdx.x;
         uint32_t asked = 0, item = 0;
         ItemScan scan;
         bool more = true, pending = false;
         while (more) {
-            const int unit = x / packed_heads, h0 = (x - unit * packed_heads) * p.pack;
+            int unit, h0;
+            p.order.at(x, unit, h0);
+            h0 *= p.pack;
             bool ok = true;
             // a block stands for item `unit`; with split keys, where the grid is an estimate, also for every
             // units-th one after it
@@ -739,9 +741,11 @@ VarlenFwdPlan varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv) {
     const long long tiles = varlen::tile_bound(N, Tq, pk), ctas = tiles * (H / pk);
     const long long blocks = (static_cast<long long>(Tk) + varlen::BN - 1) / varlen::BN;
     const bool single = static_cast<long long>(Tq) <= static_cast<long long>(N) * (varlen::BM / pk);
-    VarlenFwdPlan plan{pk, 0, single ? 1 : 0, 1, tiles};
+    VarlenFwdPlan plan{pk, 0, single ? 1 : 0, 1, tiles, {}};
+    if (ctas == 0) return plan;
+    plan.order = head_order(tiles, H / pk, 512.0 * Tk * Hkv);
     const long long want = (single ? 4 : 2) * 148;
-    if (ctas == 0 || ctas >= want || N > SPLIT_N) return plan;
+    if ( ctas >= want || N > SPLIT_N) return plan;
     // key blocks that one head's items walk in all: a sequence's once for every tile of its queries
     const long long walked = single ? blocks : blocks * ((tiles + N - 1) / N);
     const long long items = (want + H / pk - 1) / (H / pk);            // of one packed head
@@ -757,6 +761,7 @@ VarlenFwdPlan varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv) {
     plan.chunk = static_cast<int>(chunk);
     plan.parts = static_cast<int>((blocks + chunk - 1) / chunk);
     plan.units = walked / chunk + tiles;
+    plan.order = head_order(plan.units, H / pk, 512.0 * Tk * Hkv);
     return plan;
 }
 

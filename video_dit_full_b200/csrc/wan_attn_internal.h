@@ -82,12 +82,39 @@ struct VarlenParams {
     unsigned long long wait_budget_ns;
     int* status;
 };
+// The order in which a packed kernel's blocks take (unit, head) pairs, units being a head's items, longest
+// first.  Head by head, the blocks of a wave share a head's keys (or queries) in L2; with all heads in turn, the
+// longest units of every head start first and the blocks end together.  So the first heads go in groups of about
+// one wave, the last ones in one group of three; all in one where what they share fits L2 anyway.
+struct HeadOrder {
+    int units, heads, group, last;    // heads to a group; heads of the last group
+#ifdef __CUDACC__
+    __device__ __forceinline__ void at(int x, int& unit, int& head) const {
+        int first = heads - last, n = last, y = x - first * units;
+        if (y < 0) {
+            const int g = x / (group * units);
+            n = min(group, first - g * group);
+            first = g * group;
+            y = x - first * units;
+        }
+        unit = y / n;
+        head = first + (y - unit * n);
+    }
+#endif
+};
+inline HeadOrder head_order(long long units, int heads, double shared_bytes) {
+    const long long wave = (148 + units - 1) / units, tail = (3 * 148 + units - 1) / units;
+    const int last = shared_bytes <= 100e6 || tail > heads ? heads : static_cast<int>(tail);
+    return {static_cast<int>(units), heads, static_cast<int>(wave < heads ? wave : heads), last};
+}
+
 struct VarlenFwdParams : VarlenParams {
     void* o;                          // bf16 [Tq, H, 128]
     float* lse;                       // fp32 [H, Tq]
     int pack;                         // query heads that share a Q tile (a divisor of H / Hkv)
     int chunk;                        // key blocks of a part where a sequence's keys are split, 0: they are not
     int streamed;                     // K and V are read about once
+    HeadOrder order;                  // of packed heads
     float* o_part;                    // workspace fp32 [most parts, Tq, H, 128], where split
     float* lse_part;                  // workspace fp32 [most parts, H, Tq] (base-2 log)
     int* parts;                       // workspace [Tq]: parts of the token's sequence
@@ -98,6 +125,7 @@ struct VarlenBwdParams : VarlenParams {
     void *dq, *dk, *dv;               // bf16, token strides below
     long long lddq, lddk, lddv;
     int splits;                       // CTAs sharing one key tile, each over its own run of Q tiles
+    HeadOrder heads;                  // of kv heads
     float* dq_acc;                    // workspace fp32 [Tq, H, 128]: unscaled dS K
     float* delta;                     // workspace fp32 [H, Tq]: rowsum(dO * O)
     float *dk_acc, *dv_acc;           // workspace fp32 [Tk, Hkv, 128], splits > 1 only
@@ -190,7 +218,8 @@ int launch_varlen_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
 struct VarlenFwdPlan {
     int pack, chunk, streamed;        // as in VarlenFwdParams
     int parts;                        // most parts of a sequence
-    long long units;                  // the grid: units x (H / pack)
+    long long units;                  // the grid: units x (H / pack), in `order`
+    HeadOrder order;
 };
 VarlenFwdPlan varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv);
 // tk, tv: boxes (64, 1, 128); tq, tdo: (64, pack, 128 / pack); tdq: fp32 [Tq, H, 128], (128, pack, 128 / pack); tdk, tdv: fp32
