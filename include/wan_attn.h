@@ -429,7 +429,7 @@ WAN_ATTN_API int wan_attn_varlen_bwd(const void* q, const void* k, const void* v
  * c = 0, so that it shows in every result that uses it)
  *     Y[m,n] = bf16(s_x[m] s_w[n] sum_k cx[m,k] cw[n,k] + bias[n])
  * with exact int32 sums.  K must be a multiple of 16, 16 <= K <= 131072 (the
- * sums' range), N a multiple of 8, M >= 0.  Code rows are K contiguous bytes;
+ * sums' range), N a multiple of 8, M >= 0 (both at most 2^31 - 2^16).  Code rows are K contiguous bytes;
  * pointers 16-byte aligned, scales 4-byte, outputs overlap no input.
  */
 /* x bf16 [M, K], ldx elements (a multiple of 8) from row to row -> codes int8 [M, K], scales fp32 [M]. */

@@ -116,6 +116,18 @@ def test_int8_calls(lib):
     assert p
 
 
+def test_int8_sizes_near_2_31(lib):
+    """Rounding such a size up to a tile would pass 32 bits."""
+    far = [ctypes.c_void_p(0x1000000000000 + i * 0x10000000000) for i in range(5)]
+    m = 0x7fffffff
+    assert lib.wan_int8_quantize_rows(*far[:3], m, 16, 16, None) == INVALID
+    assert lib.wan_int8_dequantize_rows(*far[:3], m, 16, None) == INVALID
+    assert lib.wan_int8_gemm(far[0], far[1], far[2], far[3], None, far[4], m, 8, 16, None) == INVALID
+    assert lib.wan_int8_gemm(far[0], far[1], far[2], far[3], None, far[4], 8, 0x7ffffff8, 16, None) == INVALID
+    assert lib.wan_int8_grad_weight(*far[:4], 8, 0x7ffffff8, 16, None) == INVALID
+    assert lib.wan_int8_grad_input(*far[:4], m, 8, 16, None) == INVALID
+
+
 def test_python_refuses_what_is_not_on_the_gpu(built):
     import torch
     import video_dit_full_b200 as wa

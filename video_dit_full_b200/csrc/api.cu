@@ -478,9 +478,10 @@ bool fill_packed(VarlenParams& p, const void* q, const void* k, const void* v, c
     return p.status != nullptr;
 }
 
-// Shapes of the int8 linear calls: M >= 0 rows, K % 16 == 0, 16 <= K <= 131072, N % 8 == 0 (>= 8).
+// Shapes of the int8 linear calls: M >= 0 rows, K % 16 == 0, 16 <= K <= 131072, N % 8 == 0 (>= 8); M and N leave
+// room for rounding up to a tile in 32 bits.
 int check_int8_shape(int M, int N, int K) {
-    if (M < 0 || K < 16 || (K & 15) || K > 131072 || N < 8 || (N & 7)) return WAN_ATTN_ERR_INVALID_ARG;
+    if (M > 0x7fff0000 || N > 0x7fff0000 || M < 0 || K < 16 || (K & 15) || K > 131072 || N < 8 || (N & 7)) return WAN_ATTN_ERR_INVALID_ARG;
     const double lim = double(1ull << 40);
     if (double(M) * K >= lim || double(N) * K >= lim || double(M) * N >= lim) return WAN_ATTN_ERR_INVALID_ARG;
     return WAN_ATTN_OK;

@@ -549,11 +549,10 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap tma_x, const __grid_constant
 // straight into the swizzled operand, which stays for all of the CTA's stages.  A slice is read once and kept in
 // registers (LAYER_PIECES of 8 elements a thread); the row's absmax meets through distributed shared memory.
 // Every channel tile does so again; the few tokens come from L2.  The first tile's cluster also writes the
-// checkpoint, if one is asked for.One launch less is what it
-// saves: a token of 1536 -> 1536 takes 5.3 us a call against 7.2 with a quantiser launched before the product;
-// in a graph, and where the weight's bytes take longer, the two kernels overlap as well (5120 -> 5120, weights
-// from memory: 10.0 us both; in a graph 9.3 and 9.1), and with more tokens they win (37 tokens of 1536 -> 8960:
-// 8.2 and 11.4), so it stops at 16.
+// checkpoint, if one is asked for.  One launch less is what it saves: a token of 1536 -> 1536 takes 5.3 us a call
+// against 7.2 with a quantiser launched before the product.  In a graph, and where the weight's bytes take
+// longer, the two kernels overlap as well (5120 -> 5120, weights from memory: 10.0 us both; in a graph 9.3 and
+// 9.1), and with more tokens they win (37 tokens of 1536 -> 8960: 8.2 and 11.4), so it stops at 16.
 constexpr int LAYER_TOKENS = 16, LAYER_PIECES = 8;         // pieces of the slice a thread keeps
 struct LayerCfg {
     static constexpr int A_BYTES = 128 * BK, STAGES = 5;
