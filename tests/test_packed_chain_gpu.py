@@ -81,3 +81,66 @@ def test_backward_behind_its_forward():
         for a, b in zip(g, w):
             bar = b.abs().float() * 2 ** -7 + b.float().abs().max() * 2 ** -12
             assert ((a.float() - b.float()).abs() <= bar).all()
+
+
+def small():
+    import torch
+    import video_dit_full_b200 as wa
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    new = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16)       # noqa: E731
+    cu = torch.tensor([0, 3, 200]).to(torch.int32).cuda()
+    q, kv = new(200, 4, 128), new(200, 2, 128)
+    wc, ws = wa.int8_quantize_rows(new(256, 512))
+
+    def call():
+        o, lse = wa.varlen_fwd(q, kv, kv, cu, cu, causal=True)
+        y, codes, scales = wa.int8_linear(o.view(200, 512), wc, ws, return_checkpoint=True)
+        return o, lse, y, codes, scales, wa.int8_grad_weight(y, codes, scales), wa.int8_linear(o.view(200, 512)[:9], wc, ws)
+
+    want = call()
+    torch.cuda.synchronize()
+    return call, want
+
+
+def test_threads():
+    """Calls from several threads, each on a stream of its own, at once."""
+    import threading
+
+    import torch
+    call, want = small()
+    bad = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(100):
+                got = call()
+            torch.cuda.current_stream().synchronize()
+            bad.extend(i for i, (a, b) in enumerate(zip(got, want)) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_modes_and_memory():
+    """Inference mode and parameters as arguments; what a call allocates is given back."""
+    import torch
+    import video_dit_full_b200 as wa
+    call, want = small()
+    with torch.inference_mode():
+        got = call()
+    assert got[0].is_inference() and all(torch.equal(a, b) for a, b in zip(got, want))
+    w = torch.nn.Parameter(torch.randn(64, 64, device="cuda").to(torch.bfloat16))
+    codes, scales = wa.int8_quantize_rows(w)
+    assert not codes.requires_grad and torch.equal(codes, wa.int8_quantize_rows(w.detach())[0])
+    del got
+    before = torch.cuda.memory_allocated()
+    for _ in range(50):
+        call()
+        for wrong in (lambda: wa.int8_linear(w, codes, scales[:-1]), lambda: wa.int8_quantize_rows(w[:, :40].contiguous())):
+            with pytest.raises((ValueError, wa.WanAttnError)):
+                wrong()
+    assert torch.cuda.memory_allocated() == before
