@@ -22,23 +22,32 @@ __device__ __forceinline__ float2 bf16x2_floats(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-// rint of the exact quotient 127 x / amax, half to even, as the low byte of the result.  127 x is exact in
+// rint of the exact quotients 127 x / amax, half to even, as the low bytes of the results.  127 x is exact in
 // fp32 (7 + 8 bits).  q = 127 x * inv is within an ulp of the quotient, the fma's residual 127 x - q amax is
 // exact, and one correction gives the correctly rounded quotient (Markstein's division, inv = RN(1 / amax)).
 // A quotient of these 8-bit significands that is not a half-integer is at least 2^-9 away from one, so
 // rounding it again to an integer is rounding the exact quotient; a half-integer is represented exactly.
-__device__ __forceinline__ uint32_t code_of(float x, float amax, float inv) {
-    const float a = 127.f * x;
-    const float q = a * inv;
-    const float r = fmaf(fmaf(-q, amax, a), inv, q);
-    return __float_as_uint(r + 12582912.f);                // 1.5 * 2^23: the sum's low bits are the integer
-}
+// In pairs (packed fp32): the quantiser issues as many instructions as it can hide behind memory.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, float pre, float amax, float inv) {
-    const float2 a = bf16x2_floats(lo), b = bf16x2_floats(hi);
-    const uint32_t c0 = code_of(a.x * pre, amax, inv), c1 = code_of(a.y * pre, amax, inv);
-    const uint32_t c2 = code_of(b.x * pre, amax, inv), c3 = code_of(b.y * pre, amax, inv);
-    return __byte_perm(__byte_perm(c0, c1, 0x0040), __byte_perm(c2, c3, 0x0040), 0x5410);
+    auto pair = [&](uint32_t u) {
+        const float2 a = fmul2(bf16x2_floats(u), both(127.f * pre));
+        const float2 q = fmul2(a, both(inv));
+        const float2 r = ffma2(ffma2(q, both(-amax), a), both(inv), q);
+        const float2 c = fadd2(r, both(12582912.f));       // 1.5 * 2^23: the sum's low bits are the integer
+        return __byte_perm(__float_as_uint(c.x), __float_as_uint(c.y), 0x0040);
+    };
+    return __byte_perm(pair(lo), pair(hi), 0x5410);
 }
+// |x| as bits: the largest finite magnitude orders like an integer, and an infinity or NaN above it.  Of eight
+// values, the even and the odd ones apart, with what was seen before.
+__device__ __forceinline__ uint32_t most_of(uint32_t seen, uint4 u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) asm("max.u16x2 %0, %0, %1;" : "+r"(seen) : "r"(w[e] & 0x7fff7fffu));
+    return seen;
+}
+__device__ __forceinline__ uint32_t most_of_halves(uint32_t seen) { return max(seen & 0xffffu, seen >> 16); }
 
 // What a row's absmax (as bf16 bits; an infinity or NaN is at least 0x7f80) makes of its values.
 struct RowScale {
@@ -74,20 +83,15 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __nv_bfloat16* x,
     const uint4* row = reinterpret_cast<const uint4*>(x + (here ? m : 0) * ldx);
     const int pieces = here ? K / 8 : 0;
     uint4 kept[CACHED];
-    // |x| as bits: the largest finite magnitude orders like an integer, and an infinity or NaN above it
     uint32_t amax_bits = 0;
-    auto fold = [&](uint4 u) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) amax_bits = max(amax_bits, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-    };
 #pragma unroll
     for (int c = 0; c < CACHED; ++c)
         if (c * T + tid < pieces) kept[c] = row[c * T + tid];
 #pragma unroll
     for (int c = 0; c < CACHED; ++c)
-        if (c * T + tid < pieces) fold(kept[c]);
-    for (int c = CACHED * T + tid; c < pieces; c += T) fold(row[c]);
+        if (c * T + tid < pieces) amax_bits = most_of(amax_bits, kept[c]);
+    for (int c = CACHED * T + tid; c < pieces; c += T) amax_bits = most_of(amax_bits, row[c]);
+    amax_bits = most_of_halves(amax_bits);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) amax_bits = max(amax_bits, __shfl_xor_sync(0xffffffffu, amax_bits, off));
     if (T > 32) {
@@ -631,13 +635,6 @@ layer_few_kernel(const __grid_constant__ CUtensorMap tma_w, const LayerParams p)
         return t < p.M;
     };
     auto load = [&](int t, int c) { return *reinterpret_cast<const uint4*>(p.x + t * p.ldx + c * 8); };
-    auto most_of = [](uint4 u) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        uint32_t most = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-        return most;
-    };
     // the whole warp: into the token's absmax, with one atomic where its lanes hold one token
     auto fold = [&](bool here, int t, uint32_t most) {
         const int t0 = __shfl_sync(0xffffffffu, t, 0);
@@ -667,7 +664,7 @@ layer_few_kernel(const __grid_constant__ CUtensorMap tma_w, const LayerParams p)
             if (i * C::QUANT >= p.M * pieces) break;       // the same for every thread
             int t, c;
             const bool here = piece_of(i, pieces, t, c);
-            fold(here, t, here ? most_of(kept[i]) : 0u);
+            fold(here, t, here ? most_of_halves(most_of(0u, kept[i])) : 0u);
         }
     }
     if (splits > 1) cluster_sync_all();        // the slices' absmax are there
