@@ -27,7 +27,8 @@ __device__ __forceinline__ float2 bf16x2_floats(uint32_t u) {
 // exact, and one correction gives the correctly rounded quotient (Markstein's division, inv = RN(1 / amax)).
 // A quotient of these 8-bit significands that is not a half-integer is at least 2^-9 away from one, so
 // rounding it again to an integer is rounding the exact quotient; a half-integer is represented exactly.
-// In pairs (packed fp32): the quantiser issues as many instructions as it can hide behind memory.
+// In pairs (packed fp32): one value an instruction, the quantiser's arithmetic no longer hid behind memory
+// (32760 x 5120: 97 us; 80 us and 6.3 TB/s in pairs).
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, float pre, float amax, float inv) {
     auto pair = [&](uint32_t u) {
