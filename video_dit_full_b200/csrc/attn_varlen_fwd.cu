@@ -253,7 +253,8 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
             __syncwarp();
         }
         if (pending) drain_wait(bar(CLC), asked & 1u);    // the answer must not land in memory that is gone
-        if (!*abort_flag && wait_item(bar(W_EMPTY + (item & 1u)), ((item >> 1) & 1u) ^ 1u, wc) && lane == 0) {
+        const bool stopped = __any_sync(0xffffffffu, *abort_flag != 0);      // the same on every lane: wait_item votes
+        if (!stopped && wait_item(bar(W_EMPTY + (item & 1u)), ((item >> 1) & 1u) ^ 1u, wc) && lane == 0) {
             slot_of(item)->n = -1;
             mbar_arrive(bar(W_FULL + (item & 1u)));
         }
@@ -458,8 +459,9 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
         for (;; st += 8u) {
             // the item's slot is kept until its epilogue is done: only what the loop needs is in registers
             bool ok = wait_warp(bar(W_FULL + ((st >> 3) & 1u)), (st >> 4) & 1u, wc);
-            named_bar_sync(1 + t, BM);           // the group's warps go on together or not at all:
-            if (*abort_flag) break;              // one that gave up set the flag before the barrier
+            // The group's warps go on together or not at all: a warp that gave up set the flag before the barrier.
+            // Any other role may set it at any time, so what counts is what they read before, joined.
+            if (named_bar_any(1 + t, BM, *abort_flag != 0)) break;
             uint32_t w = base + OFF_WORK + ((st >> 3) & 1u) * WORK_BYTES;
             if (WORK(w, n) < 0) break;
             const int nt = t ? WORK(w, nt[1]) : WORK(w, nt[0]);
@@ -645,8 +647,7 @@ varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant
             const int q_begin = WORK(w, q_begin), h0 = WORK(w, h0);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(W_EMPTY + ((st >> 3) & 1u)));
-            named_bar_sync(1 + t, BM);                // every warp of the group, whatever its state
-            if (*abort_flag) break;                   // a warp that gave up set it before the barrier
+            if (named_bar_any(1 + t, BM, *abort_flag != 0)) break;   // every warp of the group, whatever its state
             if (r == 0 && nt > 0) {
                 if (by_tma) {
                     tma_store_3d(&tmo, stage, 0, h0, q_begin + i_tile);
