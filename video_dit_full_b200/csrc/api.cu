@@ -814,6 +814,7 @@ int wan_attn_varlen_fwd(const void* q, const void* k, const void* v, void* o, fl
     p.chunk = plan.chunk;
     p.streamed = plan.streamed;
     p.order = plan.order;
+    p.most_parts = plan.parts;
     if (need) {
         const size_t rows = size_t(plan.parts) * Tq * H;
         char* ws = static_cast<char*>(workspace);

@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(128) varlen_join_kernel(const VarlenFwdParams 
     if (row >= rows) return;
     const int lane = threadIdx.x & 31, token = static_cast<int>(row / p.H), head = static_cast<int>(row % p.H);
     if (token < p.cu_q[0] || token >= p.cu_q[p.N]) return;       // outside every sequence
-    const int parts = p.parts[token];
+    const int parts = parts_to_join(p.parts[token], p.most_parts);
     if (parts == 1) return;                                      // the item wrote its results itself
     // the parts' weights: part z and z + 32 in lane z, then one after the other past every lane's columns
     const float* lse = p.lse_part + static_cast<long long>(head) * p.Tq + token;

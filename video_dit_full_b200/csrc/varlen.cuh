@@ -33,6 +33,9 @@ struct ItemScan {
     Span q, k;                     // this lane's sequence
     int mine, upto;                // its items; the step's up to and including it
 };
+// The join kernel's number of parts of a token's sequence, as the forward stored it.  A forward that timed out
+// may have left the workspace as it was: never more than the plan's most, and 1 (nothing to join) for no count.
+__host__ __device__ inline int parts_to_join(int stored, int most) { return stored < 1 ? 1 : stored < most ? stored : most; }
 __device__ __forceinline__ int parts_of(int len, int size) { return (len + size - 1) / size; }
 __device__ __forceinline__ void scan_step(const int* cu_q, const int* cu_k, int N, int Tq, int Tk, int rows, int keys,
                                           int n0, ItemScan& scan) {

@@ -118,6 +118,7 @@ struct VarlenFwdParams : VarlenParams {
     float* o_part;                    // workspace fp32 [most parts, Tq, H, 128], where split
     float* lse_part;                  // workspace fp32 [most parts, H, Tq] (base-2 log)
     int* parts;                       // workspace [Tq]: parts of the token's sequence
+    int most_parts;                   // that the workspace has room for
 };
 struct VarlenBwdParams : VarlenParams {
     const void *o, *dout;             // bf16 [Tq, H, 128]
