@@ -77,6 +77,29 @@ const at::Tensor& plain(const Device& dev, const char* name, PyObject* o, at::Sc
     return t;
 }
 
+// Whether a contiguous tensor of shape `a` has the elements of one of shape `b` in their order: neighbouring axes
+// joined ([T, H D] for [T, H, D]) or split, never exchanged.  Then every axis of the one ends where one of the
+// other does.
+bool same_order(at::IntArrayRef a, at::IntArrayRef b) {
+    if (c10::multiply_integers(a) == 0) return true;                       // no elements
+    const at::IntArrayRef few = a.size() < b.size() ? a : b, many = a.size() < b.size() ? b : a;
+    int64_t end = 1, at = 1;
+    size_t i = 0;
+    for (const int64_t n : few) {
+        end *= n;
+        while (at < end && i < many.size()) at *= many[i++];
+        if (at != end) return false;
+    }
+    return true;
+}
+
+// ... contiguous, of this shape or one of the same order.
+const at::Tensor& plain(const Device& dev, const char* name, PyObject* o, at::ScalarType type, at::IntArrayRef sizes) {
+    const at::Tensor& t = plain(dev, name, o, type, c10::multiply_integers(sizes));
+    TORCH_CHECK_VALUE(same_order(t.sizes(), sizes), name, " has shape ", t.sizes(), ", expected ", sizes);
+    return t;
+}
+
 // ... a matrix of `cols` columns (-1: any).
 const at::Tensor& matrix(const Device& dev, const char* name, PyObject* o, at::ScalarType type, int64_t cols = -1) {
     const at::Tensor& t = plain(dev, name, o, type);
@@ -87,7 +110,7 @@ const at::Tensor& matrix(const Device& dev, const char* name, PyObject* o, at::S
 
 // An output: the tensor given, checked, or a new one of the sizes.
 at::Tensor output(const Device& dev, const char* name, PyObject* o, at::ScalarType type, at::IntArrayRef sizes) {
-    if (o != Py_None) return plain(dev, name, o, type, c10::multiply_integers(sizes));
+    if (o != Py_None) return plain(dev, name, o, type, sizes);
     return at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, dev.index), std::nullopt);
 }
 
@@ -231,10 +254,9 @@ PyObject* varlen_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const PackedCall c(a);
     const int causal = PyObject_IsTrue(a[5]);
     if (causal < 0) throw python_error();
-    const int64_t rows = static_cast<int64_t>(c.H) * c.Tq;
-    const at::Tensor& o = plain(c.dev, "o", a[6], at::kBFloat16, rows * c.D);
-    const at::Tensor& dout = plain(c.dev, "do", a[7], at::kBFloat16, rows * c.D);
-    const at::Tensor& lse = plain(c.dev, "lse", a[8], at::kFloat, rows);
+    const at::Tensor& o = plain(c.dev, "o", a[6], at::kBFloat16, {c.Tq, c.H, c.D});
+    const at::Tensor& dout = plain(c.dev, "do", a[7], at::kBFloat16, {c.Tq, c.H, c.D});
+    const at::Tensor& lse = plain(c.dev, "lse", a[8], at::kFloat, {c.H, c.Tq});
     const Rows dq = packed_output(c.dev, "dq", a[9], c.q), dk = packed_output(c.dev, "dk", a[10], c.k),
                dv = packed_output(c.dev, "dv", a[11], c.k);
     const Workspace ws(c.dev, a[12], lib.varlen_bwd_workspace_size(c.N, c.Tq, c.Tk, c.H, c.Hkv, c.D));

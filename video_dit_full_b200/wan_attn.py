@@ -6,6 +6,9 @@ and contiguity, and their device pointers and the current CUDA stream are
 passed to the library, which runs every step of the computation in its own
 kernels.  There is no fallback: if the library is missing or a call fails, an
 exception is raised.
+
+The packed and int8 calls take a contiguous tensor also with neighbouring axes joined or split ([T, H D] for
+[T, H, D]); one whose axes come in another order is refused.
 """
 from __future__ import annotations
 
