@@ -375,9 +375,9 @@ WAN_ATTN_API int wan_attn_bwd_noalloc(const void* q, const void* k, const void* 
  *   output need no copy).  Lengths of 0 are allowed.
  * A row that sees no key gets o = 0 and lse = -inf.  Rows outside every
  * sequence are not read into any result and their o and lse are left as they
- * were.  Inside a sequence q, k, v must be finite; a row whose scores hold
- * a NaN, or +inf, gets NaN.  Offsets outside [0, T] or
- * decreasing are clipped, never followed.
+ * were.  Inside a sequence q, k, v must be finite, but for q in a row that sees
+ * no key, which meets nothing; a row whose scores hold a NaN, or +inf, gets NaN.
+ * Offsets outside [0, T] or decreasing are clipped, never followed.
  * Accumulation is fp32; P is rounded to bf16 for P V, as in wan_attn_fwd;
  * every exponential comes from the hardware exp2.  Results do not depend on
  * what else is in the batch, but for calls whose keys are split (below), where
@@ -406,8 +406,9 @@ WAN_ATTN_API int wan_attn_varlen_fwd(const void* q, const void* k, const void* v
  *              over the query heads of its group)
  *   workspace, workspace_bytes : 256-byte aligned, at least
  *              wan_attn_varlen_bwd_workspace_size bytes
- * Rows of a sequence that no query sees get zero gradients; rows outside every
- * sequence are left as they were.  dQ (and dK, dV where few key tiles make the
+ * Rows of a sequence that no query sees get zero gradients, and so do queries
+ * that see no key, whatever their q, o and dO hold (elsewhere in a sequence dO
+ * must be finite as q, k, v); rows outside every sequence are left as they were.  dQ (and dK, dV where few key tiles make the
  * call split them) is summed in fp32 in no fixed order, as in wan_attn_bwd.
  * The workspace holds an fp32 dQ accumulator [Tq, H, D], D_i [H, Tq], the key
  * tiles in the order of their work and, where split, fp32 dK and dV.

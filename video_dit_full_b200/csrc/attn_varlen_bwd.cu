@@ -29,6 +29,8 @@
 //   - rows behind the sequence in an edge tile belong to another one: K, Q and dO rows there are zeroed in
 //     shared memory before the tensor core reads them (0 x NaN is NaN), and what is added into their
 //     dQ, dK, dV accumulators is exactly zero
+//   - rows that see no key (causal, more queries than keys) are zeroed there too: their dO, a gradient at
+//     o = 0, is often not finite
 //   - few key tiles: gridDim.z CTAs split a tile's Q tiles and add dK, dV into fp32 accumulators
 #include <cuda.h>
 
@@ -119,10 +121,10 @@ struct Walk {
     }
 };
 
-// One warp: zero rows [first, 128) of a tile (two halves of d, a row 128 bytes of each).
-__device__ __forceinline__ void zero_rows(uint32_t tile, int first, int lane) {
+// One warp: zero rows [first, end) of a tile (two halves of d, a row 128 bytes of each).
+__device__ __forceinline__ void zero_rows(uint32_t tile, int first, int end, int lane) {
     for (int half = 0; half < 2; ++half)
-        for (int c = lane; c < (BM - first) * 8; c += 32)
+        for (int c = lane; c < (end - first) * 8; c += 32)
             st_shared_v4(tile + half * HALF_BYTES + first * 128 + c * 16, 0u, 0u, 0u, 0u);
 }
 
@@ -197,8 +199,8 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
 
     if (warp == WARP_TMA) {
         // ------------------------------ TMA producer ------------------------------
-        // The whole warp walks the tiles, lane 0 issues.  A tile with rows behind the sequence lands on
-        // EDGE; the warp zeroes those rows and only then hands the tile over.
+        // The whole warp walks the tiles, lane 0 issues.  A tile with rows behind the sequence, or rows that
+        // see no key, lands on EDGE; the warp zeroes those rows and only then hands the tile over.
         if (n > 0) {
             const int kv_rows = min(sk.len - kv0, BM);
             const uint32_t kv_bar = bar(kv_rows < BM ? EDGE : KV_FULL);
@@ -220,7 +222,7 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                 if (ok) {
                     pending = false;
                     edge = 1;
-                    zero_rows(sK, kv_rows, lane);
+                    zero_rows(sK, kv_rows, BM, lane);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(KV_FULL));
@@ -234,11 +236,14 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                 const int use = (i >> 1) & 1;
                 const int h = hk * group + (at_tile.head << pack_log2), tok0 = (i_first + at_tile.tile) * tokens;
                 const int rows = min(sq.len - tok0, tokens) << pack_log2;
+                // rows before `seen` see no key (causal, more queries than keys)
+                const int seen = p.causal ? min(max(-shift - tok0, 0), tokens) << pack_log2 : 0;
+                const bool edge_tile = rows < BM || seen > 0;
                 bool got = true;
                 if (lane == 0) got = wait_thread(bar(QDO_EMPTY + s), use ^ 1, wc);
                 ok = __shfl_sync(0xffffffffu, got ? 1 : 0, 0) != 0;
                 if (!ok) break;
-                const uint32_t fb = bar(rows < BM ? EDGE : QDO_FULL + s);
+                const uint32_t fb = bar(edge_tile ? EDGE : QDO_FULL + s);
                 if (lane == 0) {
                     mbar_arrive_expect_tx(fb, 2 * TILE_BYTES);
                     const int tok = sq.begin + tok0;
@@ -248,14 +253,16 @@ varlen_main_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                     tma_load_3d_hint(sDO(s) + HALF_BYTES, &tmdo, fb, 64, h, tok, keep);
                 }
                 __syncwarp();
-                if (rows < BM) {
+                if (edge_tile) {
                     pending = true;
                     ok = wait_warp(bar(EDGE), edge & 1, wc);
                     if (!ok) break;
                     pending = false;
                     ++edge;
-                    zero_rows(sQ(s), rows, lane);
-                    zero_rows(sDO(s), rows, lane);
+                    zero_rows(sQ(s), 0, seen, lane);
+                    zero_rows(sQ(s), rows, BM, lane);
+                    zero_rows(sDO(s), 0, seen, lane);
+                    zero_rows(sDO(s), rows, BM, lane);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(QDO_FULL + s));
