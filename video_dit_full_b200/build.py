@@ -7,7 +7,8 @@ in the WAN_ATTN_NVCC_FLAGS environment variable; use --force after changing it.
 Each ``csrc/*.cu`` is compiled to an object under ``_build/`` (skipped when
 up to date) and the objects are linked into ``video_dit_full_b200/libwan_attn.so``.
 ``csrc/bind.cpp``, the Python binding of the calls whose arguments are looked at
-in C++, is compiled with g++ against PyTorch into ``video_dit_full_b200/_bind.so``.
+in C++, is compiled with g++ against PyTorch into ``video_dit_full_b200/_bind.*.so``,
+named after the interpreter and the PyTorch that it is built for.
 """
 from __future__ import annotations
 
@@ -23,7 +24,6 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libwan_attn.so")
-BIND = os.path.join(HERE, "_bind.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -39,13 +39,16 @@ def nvcc() -> str:
 
 def build_binding(force: bool = False) -> str:
     """The CPython extension ``_bind`` (no device code; the CUDA library is not linked in)."""
-    src, header = os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "wan_attn.h")
-    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= max(os.path.getmtime(src), os.path.getmtime(header)):
-        return BIND
     import torch
+
+    from .wan_attn import binding_path
+    out = binding_path()
+    src, header = os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "wan_attn.h")
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+        return out
     at = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-    tmp = BIND + f".tmp{os.getpid()}"
+    tmp = out + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include")]
     for d in (at, os.path.join(at, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda):
@@ -54,8 +57,8 @@ def build_binding(force: bool = False) -> str:
             "-ltorch_cuda", "-ltorch_python"]
     print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
-    os.replace(tmp, BIND)
-    return BIND
+    os.replace(tmp, out)
+    return out
 
 
 def build(verbose: bool = False, force: bool = False) -> str:

@@ -17,7 +17,6 @@ import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libwan_attn.so")
-BIND_PATH = os.path.join(HERE, "_bind.so")
 
 STATUS = {0: "WAN_ATTN_OK", 1: "WAN_ATTN_ERR_INVALID_ARG", 2: "WAN_ATTN_ERR_UNSUPPORTED",
           3: "WAN_ATTN_ERR_CUDA", 4: "WAN_ATTN_ERR_TIMEOUT", 5: "WAN_ATTN_ERR_WORKSPACE"}
@@ -358,18 +357,27 @@ _BOUND = ("wan_attn_varlen_fwd_workspace_size", "wan_attn_varlen_fwd", "wan_attn
 _bound = None
 
 
+def binding_path() -> str:
+    """The file of the extension module ``_bind`` for this interpreter and this PyTorch.  It uses PyTorch's C++
+    interface, which another version lays out differently: a module built for that one has another name."""
+    import sysconfig
+
+    import torch
+    return os.path.join(HERE, f"_bind.torch{torch.__version__}.abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+                              f"{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def _binding():
     """The extension module ``_bind`` on the loaded library: the packed attention and int8 calls' checks of
-    their tensors, their outputs and the call, in C++ (raises if it has not been built)."""
+    their tensors, their outputs and the call, in C++ (raises if it has not been built for this PyTorch)."""
     global _bound
     if _bound is None:
         import importlib.machinery
         import importlib.util
-
-        import torch  # noqa: F401  (the module is linked against it)
-        if not os.path.exists(BIND_PATH):
-            raise RuntimeError(f"{BIND_PATH} is missing: run `python -m video_dit_full_b200.build`")
-        spec = importlib.util.spec_from_loader("_bind", importlib.machinery.ExtensionFileLoader("_bind", BIND_PATH))
+        path = binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: run `python -m video_dit_full_b200.build`")
+        spec = importlib.util.spec_from_loader("_bind", importlib.machinery.ExtensionFileLoader("_bind", path))
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         so = lib()
