@@ -1,5 +1,7 @@
-"""The Python binding's build (no GPU): a module built for one PyTorch is not taken for another's."""
+"""The Python binding's build (no GPU): a module built for one PyTorch is not taken for another's, and the C
+library builds without any."""
 import os
+import sys
 
 import pytest
 
@@ -39,3 +41,10 @@ def test_another_torch_gets_another_module(built, compiled, monkeypatch):
 def test_binding_loads(built):
     from video_dit_full_b200 import wan_attn
     assert wan_attn._binding().__file__ == wan_attn.binding_path()
+
+
+def test_library_builds_without_torch(built, compiled, monkeypatch, capsys):
+    from video_dit_full_b200 import build
+    monkeypatch.setitem(sys.modules, "torch", None)                # import torch raises ImportError
+    assert build.build_binding(force=True) is None and not compiled
+    assert build.build() == built and "no PyTorch" in capsys.readouterr().err

@@ -37,9 +37,14 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def build_binding(force: bool = False) -> str:
-    """The CPython extension ``_bind`` (no device code; the CUDA library is not linked in)."""
-    import torch
+def build_binding(force: bool = False) -> str | None:
+    """The CPython extension ``_bind`` (no device code; the CUDA library is not linked in).  Without PyTorch
+    there is nothing to bind for: None, and the C ABI is complete all the same."""
+    try:
+        import torch
+    except ImportError:
+        print("no PyTorch: the Python binding is not built", file=sys.stderr)
+        return None
 
     from .wan_attn import binding_path
     out = binding_path()
