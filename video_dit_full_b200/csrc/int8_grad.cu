@@ -474,9 +474,11 @@ template <bool Y_MN>
 int launch(const CUtensorMap& ta, const CUtensorMap& tc, const Params& p, cudaStream_t stream) {
     auto tiles = [&](long long n) { return ((p.rows + n - 1) / n) * ((p.cols + n - 1) / n); };
     const long long t256 = tiles(256), t128 = tiles(128);
-    // time in 256 x 256 tiles of a pair: a 128 x 128 tile takes a CTA half of one, at 70 % of the rate (it
-    // reads twice the shared memory per product)
-    if (static_cast<double>((t256 + 73) / 74) <= 0.5 / 0.7 * static_cast<double>((t128 + 147) / 148)) {
+    // A wave of 256 x 256 tiles on the pairs takes about as long as one of 128 x 128 tiles on single CTAs, which
+    // read twice the shared memory per product (4096 terms: 33 to 39 us and 30 to 35), so the fewer waves win, and
+    // the single CTAs where they are as many: 9600 x 784 in 3 waves of pairs 98 us, in 4 of CTAs 123; 2048 x 2048
+    // 39 (1 wave) and 65 (2); 5120 x 784, two waves of each, 68 and 66; 1536 x 1536, one of each, 39 and 35.
+    if ((t256 + 73) / 74 < (t128 + 147) / 148) {
         if (configure_smem(reinterpret_cast<const void*>(grad_pair_kernel<Y_MN>), SMEM_BYTES) != 0) return -1;
         return launch_dependent(grad_pair_kernel<Y_MN>, dim3(2 * static_cast<unsigned>(t256 < 74 ? t256 : 74)), NTHREADS,
                                 SMEM_BYTES, stream, 1, true, ta, tc, p);
