@@ -729,10 +729,11 @@ static long long tile_bound(int N, int Tq, int pack) {
 // chunk: keys are split when there are fewer than two tiles for every SM, into parts that make two; and when
 // the sequences are single tiles on average (generated tokens: memory bound, lengths anything), into parts that
 // make four.  Parts of one size rather than a number of parts to each sequence: 40 generated tokens of 8 kv heads
-// against 17 to 9806 keys 152 us (5.3 TB/s) against 159, 8 of 4 kv heads against 11,089 keys, one of them 8650,
-// 25 us against 52.  A part has at least 4 blocks (its prologue and epilogue take as long as two or three), there
-// are at most 64, and the partial results take no more memory than K and V, or 16 MB.  Beyond SPLIT_N sequences
-// the scheduler's scan over the offsets would take longer than an item.
+// against 17 to 9806 keys 152 us (5.3 TB/s; calls one by one with a cold L2, below the power cap: a loop of them
+// takes 165) against 159, 8 of 4 kv heads against 11,089 keys, one of them 8650, 25 us against 52.  A part has at
+// least 4 blocks (its prologue and epilogue take as long as two or three), there are at most 64, and the partial
+// results take no more memory than K and V, or 16 MB.  Beyond SPLIT_N sequences the scheduler's scan over the
+// offsets would take longer than an item.
 VarlenFwdPlan varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv) {
     constexpr int SPLIT_N = 256, MIN_CHUNK = 4;
     const int group = H / Hkv;
@@ -746,7 +747,7 @@ VarlenFwdPlan varlen_fwd_plan(int N, int Tq, int Tk, int H, int Hkv) {
     if (ctas == 0) return plan;
     plan.order = head_order(tiles, H / pk, 512.0 * Tk * Hkv);
     const long long want = (single ? 4 : 2) * 148;
-    if ( ctas >= want || N > SPLIT_N) return plan;
+    if (ctas >= want || N > SPLIT_N) return plan;
     // key blocks that one head's items walk in all: a sequence's once for every tile of its queries
     const long long walked = single ? blocks : blocks * ((tiles + N - 1) / N);
     const long long items = (want + H / pk - 1) / (H / pk);            // of one packed head

@@ -25,8 +25,9 @@ __device__ __forceinline__ float2 bf16x2_floats(uint32_t u) {
 // rint of the exact quotients 127 x / amax, half to even, as the low bytes of the results.  127 x is exact in
 // fp32 (7 + 8 bits).  q = 127 x * inv is within an ulp of the quotient, the fma's residual 127 x - q amax is
 // exact, and one correction gives the correctly rounded quotient (Markstein's division, inv = RN(1 / amax)).
-// A quotient of these 8-bit significands that is not a half-integer is at least 2^-9 away from one, so
-// rounding it again to an integer is rounding the exact quotient; a half-integer is represented exactly.
+// A quotient of these 8-bit significands that is not a half-integer stays 2^9 of fp32's half steps or more away from
+// one, in every binade (1/64768 at 127 * 255 / (253 * 2^8), next to 1/2; 2^-9 next to 126.5), so rounding it again to
+// an integer is rounding the exact quotient; a half-integer is represented exactly.
 // In pairs (packed fp32): one value an instruction, the quantiser's arithmetic no longer hid behind memory
 // (32760 x 5120: 97 us; 80 us and 6.3 TB/s in pairs).
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
@@ -818,7 +819,10 @@ int launch_dequant(const void* codes, const float* scales, void* x, int M, int K
 }  // namespace int8
 
 int launch_int8_quant_rows(const void* x, void* codes, float* scales, int M, int K, long long ldx, cudaStream_t stream) {
-    // few rows: all of a block on each, for latency; else as few threads as keep the row in registers
+    // Few rows: all of a block on each, for latency (148 rows of 5120: 8 us, 12 with 32 threads a row).  Else as
+    // few threads as keep the row in registers.  32760 rows, us with 32, 64, 128, 256 threads: of 1536 elements
+    // 31, 41, 60, 96; of 4096 78, 66, 78, 114; of 5120 98, 94, 88, 121; of 13824 397, 272, 240, 197.  Rows of 512
+    // with room for 4 pieces a thread 18 us, for 8 21.
     if (M <= 148) return int8::launch_quant<256, 4>(x, codes, scales, M, K, ldx, stream);
     if (K <= 1024) return int8::launch_quant<32, 4>(x, codes, scales, M, K, ldx, stream);
     if (K <= 2048) return int8::launch_quant<32, 8>(x, codes, scales, M, K, ldx, stream);
@@ -828,6 +832,8 @@ int launch_int8_quant_rows(const void* x, void* codes, float* scales, int M, int
 }
 
 int launch_int8_dequant_rows(const void* codes, const float* scales, void* x, int M, int K, cudaStream_t stream) {
+    // 32760 rows, us with 32, 64, 256 threads a row: of 512 elements 16, 21, 39; of 5120 84, 82, 84; of 13824 219,
+    // 217, 207
     if (K <= 2048) return int8::launch_dequant<32>(codes, scales, x, M, K, stream);
     if (K <= 8192) return int8::launch_dequant<64>(codes, scales, x, M, K, stream);
     return int8::launch_dequant<256>(codes, scales, x, M, K, stream);

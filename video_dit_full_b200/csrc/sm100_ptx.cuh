@@ -546,9 +546,10 @@ __device__ __forceinline__ void cluster_sync_all() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
-// The same without the cluster-wide release, whose fence costs about a thousand cycles: for an arrival
-// that hands over nothing the other CTA's threads read (a tile that this CTA's own tensor core reads,
-// made visible to it by fence_proxy_async_smem before).
+// The same without the cluster-wide release, whose fence costs about a thousand cycles: for an arrival that hands
+// over nothing in memory that the other CTA's threads read.  Its caller hands over tensor memory, which this CTA's
+// own tensor core reads: tcgen05.wait::st has seen those stores done, and tcgen05.fence::before_thread_sync orders
+// them before the arrival, whose default scope is then enough.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed_scope(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }

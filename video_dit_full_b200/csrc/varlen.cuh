@@ -19,10 +19,11 @@ __device__ __forceinline__ Span span_of(const int* cu, int n, int T) {
 
 // Item `target` of all sequences' items: the sequence and the item within it, or seq = -1 past the last.  A
 // sequence has an item for every `rows` of its queries (the last may have fewer) and every `keys` of its keys
-// (keys = 0: for all of its keys; one for a sequence without keys).  The whole warp calls it; 32 sequences a step, a sequence to a lane, so no table has to be built (and no extra launch
-// made) before the attention kernel.  Up to 32 sequences are taken longest first, so that the work handed
-// out last is short; more are taken as they come.  `scan` keeps the step where the last target was found:
-// targets that grow are found from there on, without reading the offsets again.
+// (keys = 0: for all of its keys; one for a sequence without keys).  The whole warp calls it; 32 sequences a
+// step, a sequence to a lane, so no table has to be built (and no extra launch made) before the attention
+// kernel.  Up to 32 sequences are taken by their number of items, most first, so that the work handed out last
+// is short; more are taken as they come.  `scan` keeps the step where the last target was found: targets that
+// grow are found from there on, without reading the offsets again.
 struct ItemAt {
     int seq, item, items;          // items: of that sequence
     Span q, k;
