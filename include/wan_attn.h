@@ -373,6 +373,8 @@ WAN_ATTN_API int wan_attn_bwd_noalloc(const void* q, const void* k, const void* 
  *   Tq, Tk, N >= 0 (N >= 1); H a multiple of Hkv; D must be 128; token strides
  *   multiples of 8, at least H D or Hkv D (slices of a fused projection's
  *   output need no copy).  Lengths of 0 are allowed.
+ *   Rows between two sequences' keys (a cache with room to grow) are a sequence
+ *   of their own, without queries: they are not read into any result.
  * A row that sees no key gets o = 0 and lse = -inf.  Rows outside every
  * sequence are not read into any result and their o and lse are left as they
  * were.  Inside a sequence q, k, v must be finite, but for q in a row that sees

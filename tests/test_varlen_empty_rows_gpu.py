@@ -37,3 +37,25 @@ def test_rows_without_keys_leave_no_trace(case, bad):
     wa.check_status()
     assert (grads[0][empty] == 0).all() and all(torch.isfinite(g).all() for g in grads)
     compare(clean, cu_q, cu_k, True, o, lse, grads)
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1, 1], [3, 70, 200, 1]])
+def test_cache_with_room_to_grow(new):
+    """Slack rows behind each sequence's keys are sequences without queries; NaN in them leaves no trace."""
+    import torch
+    import video_dit_full_b200 as wa
+    cached, room = [300, 70, 4096, 129], [100, 58, 513, 0]
+    lens_q, lens_k = [], []
+    for a, b, c in zip(new, cached, room):
+        lens_q += [a, 0]
+        lens_k += [b, c]
+    x, cu_q, cu_k = make(lens_q, lens_k, 8, 2, seed=22)
+    d, cq, ck = dev(x, cu_q, cu_k)
+    slack = torch.cat([torch.arange(cu_k[n], cu_k[n + 1]) for n in range(1, len(lens_k), 2)])
+    for name in ("k", "v"):
+        d[name][slack.cuda()] = float("nan")
+    o, lse = wa.varlen_fwd(d["q"], d["k"], d["v"], cq, ck, causal=True)
+    grads = wa.varlen_bwd(d["q"], d["k"], d["v"], o, d["do"], lse, cq, ck, causal=True)
+    wa.check_status()
+    compare(x, cu_q, cu_k, True, o, lse, grads)
+    assert (grads[1][slack.cuda()] == 0).all() and (grads[2][slack.cuda()] == 0).all()

@@ -9,6 +9,9 @@ exception is raised.
 
 The packed and int8 calls take a contiguous tensor also with neighbouring axes joined or split ([T, H D] for
 [T, H, D]); one whose axes come in another order is refused.
+
+No call records an autograd graph: arguments may require gradients, outputs never do.  The gradients are what
+the backward calls return.
 """
 from __future__ import annotations
 
