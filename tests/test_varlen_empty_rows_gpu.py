@@ -59,3 +59,15 @@ def test_cache_with_room_to_grow(new):
     wa.check_status()
     compare(x, cu_q, cu_k, True, o, lse, grads)
     assert (grads[1][slack.cuda()] == 0).all() and (grads[2][slack.cuda()] == 0).all()
+
+
+@pytest.mark.parametrize("lens_q,H", [([12000], 1), ([3000, 4097], 2), ([700, 0, 1], 40)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_queries_and_no_key_at_all(lens_q, H, causal):
+    import video_dit_full_b200 as wa
+    x, cu_q, cu_k = make(lens_q, [0] * len(lens_q), H, 1, seed=23)
+    d, cq, ck = dev(x, cu_q, cu_k)
+    o, lse = wa.varlen_fwd(d["q"], d["k"], d["v"], cq, ck, causal=causal)
+    dq, dk, dv = wa.varlen_bwd(d["q"], d["k"], d["v"], o, d["do"], lse, cq, ck, causal=causal)
+    wa.check_status()
+    assert (o == 0).all() and (lse == -float("inf")).all() and (dq == 0).all() and dk.shape == dv.shape == (0, 1, 128)

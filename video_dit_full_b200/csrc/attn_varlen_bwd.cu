@@ -723,6 +723,7 @@ int varlen_bwd_pack(int H, int Hkv) {
 // 2000 and 12 heads takes 70 us unsplit, 106 us in three; one of 4096 with 16 heads over a single kv head
 // 0.32 ms split, 1.54 ms unsplit.
 int varlen_bwd_splits(int N, int Tq, int Tk, int H, int Hkv) {
+    if (Tk == 0) return 1;               // no key tile to split
     const double ctas = static_cast<double>(varlen_bwd_tile_bound(N, Tk)) * Hkv;
     const int pack = varlen_bwd_pack(H, Hkv), tokens = varlen_bwd::BM / pack;
     const double q_tiles = static_cast<double>((static_cast<long long>(Tq) / N + tokens - 1) / tokens) * (H / Hkv / pack);
